@@ -266,6 +266,100 @@ int w4a8_mmq_static(const uint8_t *codes, const uint16_t *d_f16,
                     int64_t M, void *y, int out_dtype, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Microscaled 4-bit floating point (f4_*)                                    */
+/* ------------------------------------------------------------------------ */
+
+/* A matrix [R][K] in microscaled 4-bit floating point is
+ *   codes   uint8 [R][K/2]  e2m1 elements q, byte j of a row holding k = 2j in
+ *                           bits 0-3 and k = 2j+1 in bits 4-7.  A code is
+ *                           sign (8) and magnitude 0 .5 1 1.5 2 3 4 6 (0..7)
+ *   scales  uint8           one scale per block of consecutive k of a row
+ *   g       fp32 [1]        tensor scale (NV only)
+ * and stands for x = q * s (MX) or x = q * s * g (NV):
+ *   W4_F4_MX  blocks of 32, s = 2^(byte - 127), byte 255 = NaN (the OCP
+ *             Microscaling MXFP4 format: e8m0 scales)
+ *   W4_F4_NV  blocks of 16, s = the e4m3 number of the byte (bits 0-6; 127 =
+ *             NaN), and one fp32 scale g for the whole matrix
+ * The scale plane is stored as the tensor cores read it, in tiles of 128 rows
+ * x 4 blocks (512 bytes), row tiles outermost: the scale of row r, block b is
+ * byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
+ * (r / 128) * ceil(blocks / 4) + b / 4.  Rows and blocks that pad the last
+ * tiles hold 0.  f4_scale_bytes gives the plane's size.
+ * R >= 0, K % 32 == 0 and K <= 131072 for every entry point below. */
+typedef enum { W4_F4_MX = 0, W4_F4_NV = 1 } w4_f4_format;
+
+typedef enum { W4_IN_BF16 = 0, W4_IN_F32 = 1, W4_IN_F16 = 2 } w4_in_dtype;
+
+/* Bytes of the scale plane of an [R][K] matrix; 0 for sizes outside the format. */
+size_t f4_scale_bytes(int64_t R, int64_t K, int format);
+
+/* Tensor scale of the NV format: *g = max(amax / 2688, 2^-100), with amax the
+ * largest magnitude among the finite elements of x [R][K] (in_dtype) and
+ * 2688 = 6 * 448, so that the largest block's scale is the largest e4m3 number
+ * and its largest element the largest e2m1 number.  R == 0 or K == 0 gives
+ * 2^-100.  R <= 2^24. */
+int f4_tensor_scale(const void *x, int in_dtype, int64_t R, int64_t K, float *g,
+                    void *stream);
+
+/* Quantise x [R][K] (in_dtype) block by block, with amax the largest magnitude
+ * of the block, all arithmetic fp32 round to nearest even:
+ *   MX: e = max(floor(log2(amax)) - 2, -127), byte = e + 127,
+ *       q = e2m1(x * 2^-e); amax = 0 gives byte 0
+ *   NV: s = e4m3(amax / (6 * g)); q = e2m1(x * (1 / (s * g))), or 0 if s * g = 0
+ * where e4m3 and e2m1 round to nearest even and saturate at 448 and 6; zeros
+ * keep the sign of x.  g: device fp32 scalar in [2^-100, 2^100] for NV (from
+ * f4_tensor_scale or from calibration; elements beyond 2688 * g saturate), not
+ * read for MX (may be NULL).  A block that holds a NaN or an infinity gets
+ * codes 0 and the NaN scale.  The whole scale plane is written, padding too.
+ * R <= 2^24; R == 0 or K == 0 enqueues nothing. */
+int f4_quantize(const void *x, int in_dtype, int64_t R, int64_t K, int format,
+                const float *g, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* Inverse of f4_quantize: y [R][K] of out_dtype = (q * s) * g, fp32, rounded
+ * once more for bf16.  R <= 2^24; R == 0 or K == 0 enqueues nothing. */
+int f4_dequantize(const uint8_t *codes, const uint8_t *scales, const float *g,
+                  int64_t R, int64_t K, int format, void *y, int out_dtype,
+                  void *stream);
+
+/* Embedding lookup in a table [V][K] held in 4 bits (the tied vocabulary
+ * matrix that f4_gemv multiplies by as lm_head):
+ *   y[t][k] = (q * s)[ids[t]][k] * (g * alpha)       fp32 (MX: g = 1)
+ * ids: int64 [T]; an id outside [0, V) (padding) gives a row of zeros.
+ * V >= 1, V <= 2^24, T <= 2^24; T == 0 or K == 0 enqueues nothing. */
+int f4_embed(const uint8_t *codes, const uint8_t *scales, const float *g,
+             int64_t V, int64_t K, int format, const int64_t *ids, int64_t T,
+             float alpha, void *y, int out_dtype, void *stream);
+
+/* Product of two 4-bit matrices on the block-scaled tensor cores:
+ *   y[t][n] = gw * ga * sum_k (q * s)_w[n][k] * (q * s)_a[t][k]
+ * accumulated in fp32.  codes, scales, g: the weights [N][K]; qa, sa, ga: the
+ * activations [M][K] (f4_quantize), both of `format`; y: [M][N] of out_dtype.
+ * 1 <= M <= 2^24, 1 <= N <= 2^24, 32 <= K <= 131072.  A NaN scale makes its
+ * row or column NaN. */
+int f4_mm(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N,
+          int64_t K, int format, const uint8_t *qa, const uint8_t *sa,
+          const float *ga, int64_t M, void *y, int out_dtype, void *stream);
+
+/* Bytes of device workspace that f4_gemv needs; 0 for sizes outside its range. */
+size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format);
+
+/* Decode GEMV: y[t][n] = g * sum_k (q * s)[n][k] * x[t][k] with bf16
+ * activations x [M][K] that are not quantised to 4 bits: each block of x (32 k
+ * for MX, 16 for NV) is held in fixed point, 2^-22 of the block's largest
+ * magnitude (every element above 2^-14 of it exact), split into eight base-8
+ * digits that are e2m1 numbers, so that the block-scaled tensor cores multiply
+ * the weights as they are stored.  (NV: a block below 2^-17 of the token's
+ * largest magnitude is held at that block size.)  Accumulated in fp32.
+ * 1 <= M <= 8, 1 <= N <= 2^24, 32 <= K <= 65536, K % 32 == 0; y: [M][N] of
+ * out_dtype.  `workspace` (16-byte aligned) must hold f4_gemv_workspace_size
+ * bytes, else W4_ERR_WORKSPACE; it holds the digits, and calls that can
+ * overlap on the GPU need one each.  A token with a NaN or an infinity gives
+ * NaN outputs. */
+int f4_gemv(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N,
+            int64_t K, int format, const uint16_t *x_bf16, int M, void *y,
+            int out_dtype, void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Test entry points: they check the library's own machinery, not the method */
 /* ------------------------------------------------------------------------ */
 

@@ -22,10 +22,20 @@ Entry points (same names as the C ABI):
     w4a8_gemv_blockdots(codes, d, m, qa, dx, bsum, out_dtype) -> y, P  (test: int32 block products)
     w4a8_mmq_workspace_size(M, N, K)
     w4_check_device_error()
+Microscaled 4-bit floating point (planes codes, scales, g; g is None for the
+MX format and the fp32 tensor scale for NV):
+    f4_tensor_scale(x)                      -> g
+    f4_quantize(x, format, tensor_scale)    -> codes, scales, g
+    f4_dequantize(codes, scales, g, out_dtype) -> y
+    f4_embed(codes, scales, g, ids, scale, out_dtype) -> y   (rows of a packed table)
+    f4_mm(codes, scales, g, qa, sa, ga, out_dtype) -> y      (both operands 4-bit, any M)
+    f4_gemv(codes, scales, g, x, out_dtype) -> y             (bf16 activations, M <= 8)
+    f4_gemv_workspace_size(M, N, K, format)
 """
 from __future__ import annotations
 
-from ._lib import (LibraryMissing, W4_OK, W4_OUT_BF16, W4_OUT_F32, load, status_string)
+from ._lib import (LibraryMissing, W4_F4_MX, W4_F4_NV, W4_IN_BF16, W4_IN_F16, W4_IN_F32, W4_OK,
+                   W4_OUT_BF16, W4_OUT_F32, load, status_string)
 
 __all__ = [
     "W4Error", "LibraryMissing", "w4_pack", "w4_pack_g32", "w4_pack_codes", "w4_unpack",
@@ -33,6 +43,8 @@ __all__ = [
     "w4a8_gemv_bf16",
     "q8_quantize_act", "w4a8_mmq", "w4a8_mmq_static", "w4a8_mmq_workspace_size",
     "w4a8_mmq_blockdots", "w4a8_gemv_blockdots",
+    "f4_tensor_scale", "f4_quantize", "f4_dequantize", "f4_embed", "f4_mm", "f4_gemv",
+    "f4_gemv_workspace_size",
     "w4_check_device_error",
     "w4_abi_version", "lib",
 ]
@@ -393,3 +405,203 @@ def w4a8_gemv_blockdots(codes, d, m, qa, dx, bsum, out_dtype=None, y=None, strea
                                       _stream(stream)), "w4a8_gemv_blockdots")
     return y, P
 
+
+
+# ---------------------------------------------------------------------------
+# microscaled 4-bit floating point
+# ---------------------------------------------------------------------------
+
+F4_FORMATS = {"mx": W4_F4_MX, "nv": W4_F4_NV}
+F4_BLOCK = {W4_F4_MX: 32, W4_F4_NV: 16}
+
+
+def _f4_format(format) -> int:
+    if format in F4_FORMATS:
+        return F4_FORMATS[format]
+    raise ValueError(f"unknown format {format!r}, expected one of {sorted(F4_FORMATS)}")
+
+
+def _in_code(x, name: str) -> int:
+    torch = _torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    codes = {torch.bfloat16: W4_IN_BF16, torch.float32: W4_IN_F32, torch.float16: W4_IN_F16}
+    if x.dtype not in codes:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    return codes[x.dtype]
+
+
+def _stream_on(stream, like):
+    """The stream the call runs on: the caller's, which must belong to the
+    tensors' device, or the current one."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.current_stream()
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+    return stream
+
+
+def _new(shape, dtype, like, stream):
+    """An uninitialised tensor that belongs to the stream the call runs on: the
+    allocator then hands its memory out again only in that stream's order."""
+    torch = _torch()
+    if stream == torch.cuda.current_stream():
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _f4_scale_shape(R, K: int, format: int):
+    """Shape of the scale plane (row tiles, tiles along K, bytes); an extent
+    that does not follow from the arguments is open."""
+    tiles = -(-K // (4 * F4_BLOCK[format])) if K % 32 == 0 else None
+    return (None if R is None else -(-R // 128), tiles, 512)
+
+
+def _f4_planes(codes, scales, g, names, K=None):
+    """Check the planes of one 4-bit matrix; returns rows, K, format."""
+    torch = _torch()
+    cn, sn, gn = names
+    _need(codes, torch.uint8, cn, (None, None if K is None else _div(K, 2)))
+    R, K = codes.shape[0], codes.shape[1] * 2 if K is None else K
+    format = W4_F4_MX if g is None else W4_F4_NV
+    _need(scales, torch.uint8, sn, _f4_scale_shape(R, K, format))
+    if g is not None:
+        _need(g, torch.float32, gn, (1,))
+    return R, K, format
+
+
+def _placed(**tensors):
+    """_on_device for those arguments that are present."""
+    _on_device(**{k: t for k, t in tensors.items() if t is not None})
+
+
+def _opt(t):
+    return None if t is None else _ptr(t)
+
+
+def f4_tensor_scale(x, g=None, stream=None):
+    """Tensor scale of the NV format, max(amax / 2688, 2^-100) over the finite
+    elements of x[R,K] (bf16, fp16 or fp32), as an fp32 tensor [1]."""
+    torch = _torch()
+    ic = _in_code(x, "x")
+    _need(x, x.dtype, "x", (None, None))
+    if g is not None:
+        _need(g, torch.float32, "g", (1,))
+    _placed(x=x, g=g)
+    st = _stream_on(stream, x)
+    if g is None:
+        g = _new((1,), torch.float32, x, st)
+    _check(load().f4_tensor_scale(_ptr(x), ic, x.shape[0], x.shape[1], _ptr(g), _stream(st)),
+           "f4_tensor_scale")
+    return g
+
+
+def f4_quantize(x, format="mx", tensor_scale=None, codes=None, scales=None, stream=None):
+    """x[R,K] (bf16, fp16 or fp32; K % 32 == 0) -> 4-bit planes (codes
+    uint8[R,K/2], scales uint8[ceil(R/128), ceil(K/(4*block)), 512], g).
+    format: "mx" (blocks of 32, power-of-two scales; g is None) or "nv" (blocks
+    of 16, e4m3 scales, g fp32[1]: `tensor_scale`, or found from x when
+    omitted)."""
+    torch = _torch()
+    fc, ic = _f4_format(format), _in_code(x, "x")
+    _need(x, x.dtype, "x", (None, None))
+    R, K = x.shape
+    if tensor_scale is not None:
+        if fc == W4_F4_MX:
+            raise ValueError("tensor_scale belongs to the nv format")
+        _need(tensor_scale, torch.float32, "tensor_scale", (1,))
+    shape = _f4_scale_shape(R, K, fc)
+    if codes is not None:
+        _need(codes, torch.uint8, "codes", (R, _div(K, 2)))
+    if scales is not None:
+        _need(scales, torch.uint8, "scales", shape)
+    _placed(x=x, tensor_scale=tensor_scale, codes=codes, scales=scales)
+    st = _stream_on(stream, x)
+    if codes is None:
+        codes = _new((R, K // 2), torch.uint8, x, st)
+    if scales is None:
+        scales = _new((shape[0], shape[1] or 0, 512), torch.uint8, x, st)
+    g = tensor_scale
+    if fc == W4_F4_NV and g is None:
+        g = f4_tensor_scale(x, stream=st)
+    _check(load().f4_quantize(_ptr(x), ic, R, K, fc, _opt(g), _ptr(codes), _ptr(scales),
+                              _stream(st)), "f4_quantize")
+    return codes, scales, g
+
+
+def f4_dequantize(codes, scales, g, out_dtype=None, y=None, stream=None):
+    """The values y[R,K] that 4-bit planes stand for, bf16 (default) or fp32."""
+    R, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
+    oc = _out_code(out_dtype, y)
+    y, st = _f4_output(y, R, K, oc, stream, codes=codes, scales=scales, g=g)
+    _check(load().f4_dequantize(_ptr(codes), _ptr(scales), _opt(g), R, K, fc, _ptr(y), oc,
+                                _stream(st)), "f4_dequantize")
+    return y
+
+
+def _f4_output(y, M: int, N: int, oc: int, stream, **placed):
+    """The caller's y checked, or a new one on the call's stream; the stream."""
+    torch = _torch()
+    dtype = torch.float32 if oc == W4_OUT_F32 else torch.bfloat16
+    if y is not None:
+        _need(y, dtype, "y", (M, N))
+    _placed(y=y, **placed)
+    like = next(t for t in placed.values() if t is not None)
+    st = _stream_on(stream, like)
+    return (_new((M, N), dtype, like, st) if y is None else y), st
+
+
+def f4_embed(codes, scales, g, ids, scale=1.0, out_dtype=None, y=None, stream=None):
+    """Embedding lookup: y[t] = scale * row ids[t] of the 4-bit table, for
+    ids int64[T]; an id outside the table (padding) gives a row of zeros."""
+    torch = _torch()
+    V, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
+    _need(ids, torch.int64, "ids", (None,))
+    T = ids.shape[0]
+    oc = _out_code(out_dtype, y)
+    y, st = _f4_output(y, T, K, oc, stream, codes=codes, scales=scales, g=g, ids=ids)
+    _check(load().f4_embed(_ptr(codes), _ptr(scales), _opt(g), V, K, fc, _ptr(ids), T,
+                           float(scale), _ptr(y), oc, _stream(st)), "f4_embed")
+    return y
+
+
+def f4_mm(codes, scales, g, qa, sa, ga, out_dtype=None, y=None, stream=None):
+    """y[M,N] = A W^T from 4-bit weight planes (codes, scales, g) of W[N,K] and
+    4-bit activation planes (qa, sa, ga) of A[M,K], both of one format
+    (f4_quantize), on the block-scaled tensor cores."""
+    N, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
+    if (g is None) != (ga is None):
+        raise ValueError("g and ga must both be given (nv) or both be None (mx)")
+    M, _, _ = _f4_planes(qa, sa, ga, ("qa", "sa", "ga"), K)
+    oc = _out_code(out_dtype, y)
+    y, st = _f4_output(y, M, N, oc, stream, codes=codes, scales=scales, g=g, qa=qa, sa=sa, ga=ga)
+    _check(load().f4_mm(_ptr(codes), _ptr(scales), _opt(g), N, K, fc, _ptr(qa), _ptr(sa),
+                        _opt(ga), M, _ptr(y), oc, _stream(st)), "f4_mm")
+    return y
+
+
+def f4_gemv_workspace_size(M: int, N: int, K: int, format="mx") -> int:
+    return int(load().f4_gemv_workspace_size(M, N, K, _f4_format(format)))
+
+
+def f4_gemv(codes, scales, g, x, out_dtype=None, y=None, workspace=None, stream=None):
+    """y[M,N] = x[M,K] W^T for 1 <= M <= 8 from 4-bit weight planes and bf16
+    activations (not quantised to 4 bits).  workspace: optional uint8 1-D device
+    tensor of at least f4_gemv_workspace_size(M, N, K, format) bytes (allocated
+    here when omitted)."""
+    torch = _torch()
+    _need(x, torch.bfloat16, "x", (None, None))
+    M, K = x.shape
+    N, _, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"), K)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace", (None,))
+    oc = _out_code(out_dtype, y)
+    y, st = _f4_output(y, M, N, oc, stream, codes=codes, scales=scales, g=g, x=x,
+                       workspace=workspace)
+    if workspace is None:
+        workspace = _new((int(load().f4_gemv_workspace_size(M, N, K, fc)),), torch.uint8, x, st)
+    _check(load().f4_gemv(_ptr(codes), _ptr(scales), _opt(g), N, K, fc, _ptr(x), M, _ptr(y), oc,
+                          _ptr(workspace), workspace.numel(), _stream(st)), "f4_gemv")
+    return y

@@ -26,6 +26,11 @@ W4_ERR_TIMEOUT = 7
 W4_ERR_BOUNDS = 8
 W4_OUT_BF16 = 0
 W4_OUT_F32 = 1
+W4_F4_MX = 0
+W4_F4_NV = 1
+W4_IN_BF16 = 0
+W4_IN_F32 = 1
+W4_IN_F16 = 2
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -49,6 +54,14 @@ SIGNATURES = {
     "w4a8_mmq": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _INT, _P, ctypes.c_size_t, _P],
                  _INT),
     "w4a8_mmq_static": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _INT, _P], _INT),
+    "f4_scale_bytes": ([_I64, _I64, _INT], ctypes.c_size_t),
+    "f4_tensor_scale": ([_P, _INT, _I64, _I64, _P, _P], _INT),
+    "f4_quantize": ([_P, _INT, _I64, _I64, _INT, _P, _P, _P, _P], _INT),
+    "f4_dequantize": ([_P, _P, _P, _I64, _I64, _INT, _P, _INT, _P], _INT),
+    "f4_embed": ([_P, _P, _P, _I64, _I64, _INT, _P, _I64, ctypes.c_float, _P, _INT, _P], _INT),
+    "f4_mm": ([_P, _P, _P, _I64, _I64, _INT, _P, _P, _P, _I64, _P, _INT, _P], _INT),
+    "f4_gemv_workspace_size": ([_I64, _I64, _I64, _INT], ctypes.c_size_t),
+    "f4_gemv": ([_P, _P, _P, _I64, _I64, _INT, _P, _INT, _P, _INT, _P, ctypes.c_size_t, _P], _INT),
     "w4_test_wait_expiry": ([ctypes.c_uint64, _P], _INT),
     "w4a8_gemv_blockdots": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _INT, _P, _INT, _P,
                              ctypes.c_size_t, _P], _INT),

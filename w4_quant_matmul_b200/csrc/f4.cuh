@@ -1,0 +1,54 @@
+// f4.cuh -- the microscaled 4-bit floating-point format shared by the f4_*
+// translation units: scale-plane geometry, scale bytes, host argument checks.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace f4 {
+
+constexpr int64_t kMaxK = 131072;
+constexpr int64_t kMaxRows = int64_t(1) << 24;
+
+constexpr int kRowTile = 128;    // rows of a scale tile
+constexpr int kTileBytes = 512;  // 128 rows x 4 blocks
+
+// Elements of k that share a scale, by format.
+__host__ __device__ constexpr int block_of(int fmt) { return fmt == W4_F4_MX ? 32 : 16; }
+
+// Scale tiles along K (4 blocks each).
+__host__ __device__ constexpr int64_t scale_tiles_k(int64_t K, int fmt) {
+    return (K / block_of(fmt) + 3) / 4;
+}
+
+__host__ __device__ constexpr int64_t row_tiles(int64_t R) {
+    return (R + kRowTile - 1) / kRowTile;
+}
+
+// Byte offset, in its scale plane, of the 4-byte word that holds blocks
+// 4 * kt ... 4 * kt + 3 of row r.
+__device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kt, int64_t tiles_k) {
+    return ((r >> 7) * tiles_k + kt) * kTileBytes + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+}
+
+// fp32 value of a scale byte.
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    if constexpr (FMT == W4_F4_MX) {
+        // 2^(byte - 127): the byte is the fp32 exponent; 0 is the subnormal
+        // 2^-127 and 255 NaN
+        return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
+    } else {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
+        return __half2float(__half(h));
+    }
+}
+
+// Host checks of a format and an out_dtype.
+inline bool known_format(int fmt) { return fmt == W4_F4_MX || fmt == W4_F4_NV; }
+inline bool known_out(int t) { return t == W4_OUT_BF16 || t == W4_OUT_F32; }
+inline bool known_in(int t) { return t == W4_IN_BF16 || t == W4_IN_F32 || t == W4_IN_F16; }
+
+}  // namespace f4

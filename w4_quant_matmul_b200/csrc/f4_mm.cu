@@ -1,0 +1,836 @@
+// f4_mm.cu -- products with matrices in microscaled 4-bit floating point on the
+// block-scaled tensor cores (tcgen05.mma kind::mxf4 / kind::mxf4nvf4).
+//
+//   f4_mm    y[t][n] = gw ga sum_k (q s)_w[n][k] (q s)_a[t][k]
+//   f4_gemv  y[t][n] = g sum_k (q s)[n][k] x[t][k],  x bf16, at most 8 tokens
+//
+// Both run one kernel.  A tile is 128 weight rows (the MMA's M, TMEM lanes) by
+// BN tokens (its N, TMEM columns); K advances in stages of 256 elements (128
+// bytes of codes a row, one 128B-swizzle atom), four MMAs of K = 64 each.
+//   warp 0     TMA producer: the code tiles of weights and tokens and their
+//              scale tiles into a ring of shared-memory stages.
+//   warp 1     allocates TMEM; one lane copies each stage's scale tiles to TMEM
+//              (tcgen05.cp: the scale planes are stored as the copy wants them)
+//              and issues the MMAs.  tcgen05.cp and tcgen05.mma of one thread
+//              run in issue order.
+//   warps 2-5  epilogue: TMEM -> registers -> y; a thread owns one weight row,
+//              so a warp's stores of one token are contiguous.
+// When the tiles do not fill the GPU, a cluster of up to 8 CTAs splits a tile's
+// K; each CTA leaves its fp32 partial tile in shared memory and the CTAs sum
+// them through distributed shared memory in CTA order (deterministic, and no
+// workspace).  Otherwise CTAs are persistent and the accumulators are double
+// buffered, where TMEM holds two.
+//
+// f4_gemv keeps x exact to 22 bits of each block's largest magnitude without
+// leaving the 4-bit tensor cores: a first kernel writes x as fixed point in
+// eight base-8 digits -4..3, every one of them an e2m1 number, and digit j of
+// token t becomes row 8 t + j of the token operand, with the block's power of
+// two as its scale.  The epilogue sums a token's 8 columns with weights 8^-j.
+// The weights are read once, whatever the number of tokens, and no CUDA core
+// touches them.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "f4.cuh"
+
+namespace {
+
+constexpr int BM = 128;   // weight rows of a tile
+constexpr int BK = 256;   // k of a stage
+constexpr int kRowBytes = BK / 2;
+constexpr int kMmaK = 64;
+constexpr int kThreads = 192;
+constexpr int kEpiWarp0 = 2;
+constexpr int kEpiThreads = 128;
+constexpr int kDigits = 8;      // base-8 digits of an activation
+constexpr int kMaxTokens = 8;   // f4_gemv
+constexpr int kMaxSplit = 8;    // CTAs of a cluster that share a tile's K
+constexpr size_t kSmemMax = 227 * 1024;
+constexpr size_t kSmemTwo = 113 * 1024;  // of each of two CTAs on an SM (228 KB, 1 KB reserved a CTA)
+
+// Everything that depends on the format and the tile's tokens.
+template <int FMT, int BN>
+struct Cfg {
+    static constexpr int chunks = BK / (4 * f4::block_of(FMT));  // scale tiles of a stage
+    static constexpr int mma_per_chunk = 4 / chunks;             // 2 (MX) or 1 (NV)
+    static constexpr int b_row_tiles = (BN + 127) / 128;
+    static constexpr int a_bytes = BM * kRowBytes;
+    static constexpr int b_bytes = BN * kRowBytes;
+    static constexpr int sa_bytes = chunks * f4::kTileBytes;
+    static constexpr int sb_bytes = b_row_tiles * chunks * f4::kTileBytes;
+    static constexpr int stage_bytes = a_bytes + b_bytes + sa_bytes + sb_bytes;
+    // small tiles leave room for a second CTA on the SM
+    static constexpr int stages = BN == 64 ? (FMT == W4_F4_MX ? 4 : 3) : BN == 128 ? 5 : 4;
+    static constexpr int acc_stages = BN <= 128 ? 2 : 1;
+    static constexpr int sf_cols = chunks * 4 * (1 + b_row_tiles);  // TMEM columns per slot
+    static constexpr int sf_slots = 2;
+    static constexpr int used_cols = acc_stages * (BN < 32 ? 32 : BN) + sf_slots * sf_cols;
+    static constexpr int tmem_cols =
+        used_cols <= 64 ? 64 : used_cols <= 128 ? 128 : used_cols <= 256 ? 256 : 512;
+    static constexpr int acc_cols = BN < 32 ? 32 : BN;
+    static constexpr int nbars = 2 * stages + 2 * acc_stages + 1;
+    static constexpr int bars = stages * stage_bytes;
+    static constexpr int misc = bars + nbars * 8;
+    static constexpr size_t total = (size_t)misc + 16 + 1024;
+    static_assert(used_cols <= 512, "TMEM has 512 columns");
+    static_assert(stage_bytes % 1024 == 0, "operand tiles start on swizzle atoms");
+    static_assert(total <= kSmemMax, "shared memory of one CTA");
+    static_assert((size_t)BN * BM * 4 <= (size_t)stages * stage_bytes || BN > 128,
+                  "a partial tile fits the ring");
+};
+
+struct Params {
+    const uint8_t* sa;  // weight scales
+    const uint8_t* sb;  // token scales
+    const float* gw;    // NV: tensor scales (token: f4_mm only)
+    const float* ga;
+    const float* row_factor;  // f4_gemv: factor of each token
+    void* y;
+    int M, N;          // tokens, weight rows
+    int b_rows;        // rows of the token operand
+    int K;
+    int stages_k;      // ceil(K / BK)
+    int tiles_k;       // scale tiles along K
+    int tiles_n, tiles_m;
+    int splits;
+    int out_f32;
+    int* err;
+};
+
+// ---------------------------------------------------------------------------
+// tcgen05 and cluster wrappers
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// K-major operand tile, 128-byte swizzle: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Scale tile: 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) |
+           ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// One 512-byte scale tile -> 4 TMEM columns (row r in lane r % 32 of every lane
+// quarter, column r / 32; the word's bytes are the row's 4 blocks).
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (FMT == W4_F4_MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// Instruction descriptor: e2m1 operands, K-major, M = 128, N = BN; scale type
+// e8m0 (MX) or e4m3 (NV); `id` is the byte of the scale word that the MMA's
+// first block uses (0 or 2).
+template <int FMT, int BN>
+__device__ __forceinline__ uint32_t instr_desc(int id) {
+    return ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
+           ((FMT == W4_F4_MX ? 1u : 0u) << 23) | ((uint32_t)(BM >> 7) << 27) |
+           ((uint32_t)id << 29);
+}
+
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            w4::smem_u32(bar))
+        : "memory");
+}
+
+// 16 consecutive columns of this warp's 32 lanes; the wait names the
+// registers, so that no use moves above it.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_y(const Params& p, int64_t t, int n, float v) {
+    const int64_t at = t * p.N + n;
+    if (!W4_CHECK(t >= 0 && t < p.M && n >= 0 && n < p.N, p.err)) return;
+    if (p.out_f32)
+        static_cast<float*>(p.y)[at] = v;
+    else
+        static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// kernel
+// ---------------------------------------------------------------------------
+
+// GEMV: the token operand holds digit rows (8 per token) that the preceding
+// kernel wrote; otherwise one row per token.
+template <int FMT, int BN, bool GEMV>
+__global__ void __launch_bounds__(kThreads)
+    f4_mm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                 const Params p) {
+    using C = Cfg<FMT, BN>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);  // stage loaded     [stages]
+    uint64_t* empty = full + C::stages;                            // stage consumed   [stages]
+    uint64_t* afull = empty + C::stages;                           // tile accumulated [acc_stages]
+    uint64_t* aempty = afull + C::acc_stages;                      // tile read out    [acc_stages]
+    uint64_t* drain = aempty + C::acc_stages;                      // last MMA complete
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::misc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int tiles = p.tiles_n * p.tiles_m;
+    const int split = p.splits > 1 ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
+    // this CTA's stages of every tile
+    const int kb = (int)((int64_t)p.stages_k * split / p.splits);
+    const int ke = (int)((int64_t)p.stages_k * (split + 1) / p.splits);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::stages; ++i) {
+            w4::mbar_init(&full[i], 1);
+            w4::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::acc_stages; ++i) {
+            w4::mbar_init(&afull[i], 1);
+            w4::mbar_init(&aempty[i], kEpiThreads / 32);
+        }
+        w4::mbar_init(drain, 1);
+        *abort_flag = 0;
+        w4::fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         w4::smem_u32((const void*)tmem_slot)),
+                     "r"(C::tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (w4::elect_one()) {
+            w4::prefetch_tmap(&tm_a);
+            w4::prefetch_tmap(&tm_b);
+            const int chunks_last = p.tiles_k - (p.stages_k - 1) * C::chunks;
+            auto chunks_of = [&](int ks) { return ks + 1 < p.stages_k ? C::chunks : chunks_last; };
+            auto load_a = [&](int s, int ks, int tn) {
+                const int ch = chunks_of(ks);
+                w4::mbar_arrive_expect_tx(
+                    &full[s], C::a_bytes + C::b_bytes + ch * f4::kTileBytes * (1 + C::b_row_tiles));
+                uint8_t* st = smem + s * C::stage_bytes;
+                w4::tma_load_2d(st, &tm_a, &full[s], ks * kRowBytes, tn * BM);
+                w4::bulk_load_1d(st + C::a_bytes + C::b_bytes,
+                                 p.sa + ((int64_t)tn * p.tiles_k + (int64_t)ks * C::chunks) *
+                                            f4::kTileBytes,
+                                 (uint32_t)(ch * f4::kTileBytes), &full[s]);
+            };
+            auto load_b = [&](int s, int ks, int tm) {
+                const int ch = chunks_of(ks);
+                uint8_t* st = smem + s * C::stage_bytes;
+                w4::tma_load_2d(st + C::a_bytes, &tm_b, &full[s], ks * kRowBytes, tm * BN);
+                // row tiles of the token scales; one past the last reads the last again
+                const int last = (p.b_rows - 1) / f4::kRowTile;
+#pragma unroll
+                for (int rt = 0; rt < C::b_row_tiles; ++rt) {
+                    int tile = tm * C::b_row_tiles + rt;
+                    if (tile > last) tile = last;
+                    w4::bulk_load_1d(st + C::a_bytes + C::b_bytes + C::sa_bytes +
+                                         rt * C::chunks * f4::kTileBytes,
+                                     p.sb + ((int64_t)tile * p.tiles_k + (int64_t)ks * C::chunks) *
+                                                f4::kTileBytes,
+                                     (uint32_t)(ch * f4::kTileBytes), &full[s]);
+                }
+            };
+            int it = 0;  // stages issued
+            bool ok = true;
+            // f4_gemv: the weights do not depend on the digit kernel that
+            // precedes this one, so the first stages' are requested before the
+            // wait for it (that kernel starts this one only after everything
+            // before it has completed)
+            int pre = 0;
+            if constexpr (GEMV) {
+                if (first < tiles) pre = ke - kb < C::stages ? ke - kb : C::stages;
+                for (int i = 0; i < pre; ++i) load_a(i, kb + i, first % p.tiles_n);
+            }
+            pdl_wait();
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                const int tn = GEMV ? tile : tile / p.tiles_m;
+                const int tm = GEMV ? 0 : tile % p.tiles_m;
+                (void)W4_CHECK(tn < p.tiles_n && tm < p.tiles_m && kb < ke, p.err);
+                for (int ks = kb; ks < ke; ++ks, ++it) {
+                    const int s = it % C::stages;
+                    if (it >= pre) {
+                        if (!w4::mbar_wait(&empty[s], ((uint32_t)(it / C::stages) & 1u) ^ 1u,
+                                           abort_flag, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        load_a(s, ks, tn);
+                    }
+                    load_b(s, ks, tm);
+                }
+            }
+            // drain: every issued load must land before the CTA exits
+            for (int k = it - C::stages < 0 ? 0 : it - C::stages; k < it; ++k)
+                w4::mbar_wait(&full[k % C::stages], (uint32_t)(k / C::stages) & 1u, nullptr, p.err);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (w4::elect_one()) {
+            const uint32_t sf0 = tmem + C::acc_stages * C::acc_cols;
+            int it = 0, ti = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step, ++ti) {
+                const int as = ti % C::acc_stages;
+                const uint32_t d = tmem + as * C::acc_cols;
+                if (!w4::mbar_wait(&aempty[as], ((uint32_t)(ti / C::acc_stages) & 1u) ^ 1u,
+                                   abort_flag, p.err))
+                    break;
+                tc_fence_after();
+                for (int ks = kb; ks < ke; ++ks, ++it) {
+                    const int s = it % C::stages;
+                    if (!w4::mbar_wait(&full[s], (uint32_t)(it / C::stages) & 1u, abort_flag,
+                                       p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = w4::smem_u32(smem + s * C::stage_bytes);
+                    const uint32_t b = a + C::a_bytes;
+                    const uint32_t sa = b + C::b_bytes;
+                    const uint32_t sb = sa + C::sa_bytes;
+                    const uint32_t sf = sf0 + (it % C::sf_slots) * C::sf_cols;
+                    const uint32_t sfb = sf + C::chunks * 4;
+                    // K = 64 steps of this stage that hold elements
+                    int steps = (p.K - ks * BK + kMmaK - 1) / kMmaK;
+                    if (steps > BK / kMmaK) steps = BK / kMmaK;
+#pragma unroll
+                    for (int c = 0; c < C::chunks; ++c) {
+                        if (c * C::mma_per_chunk >= steps) break;
+                        copy_scales(sf + c * 4, scale_desc(sa + c * f4::kTileBytes));
+#pragma unroll
+                        for (int rt = 0; rt < C::b_row_tiles; ++rt)
+                            copy_scales(sfb + (c * C::b_row_tiles + rt) * 4,
+                                        scale_desc(sb + (rt * C::chunks + c) * f4::kTileBytes));
+                    }
+#pragma unroll
+                    for (int j = 0; j < BK / kMmaK; ++j) {
+                        if (j >= steps) break;
+                        const int c = j / C::mma_per_chunk;
+                        const int id = j % C::mma_per_chunk * 2;
+                        mma_f4<FMT>(d, operand_desc(a + j * (kMmaK / 2)),
+                                    operand_desc(b + j * (kMmaK / 2)), instr_desc<FMT, BN>(id),
+                                    sf + c * 4, sfb + c * C::b_row_tiles * 4,
+                                    ks > kb || j > 0);
+                    }
+                    mma_commit(&empty[s]);
+                }
+                if (ok) mma_commit(&afull[as]);
+            }
+            // drain: nothing may still write TMEM or read shared memory
+            mma_commit(drain);
+            w4::mbar_wait(drain, 0u, nullptr, p.err);
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int quarter = warp & 3;  // the TMEM lanes this warp may read
+        const int row = quarter * 32 + lane;
+        float alpha = 1.0f;
+        float* part = reinterpret_cast<float*>(smem);  // split K: [column][128] in the ring
+        pdl_wait();
+        if constexpr (FMT == W4_F4_NV) alpha = GEMV ? __ldg(p.gw) : __fmul_rn(__ldg(p.gw), __ldg(p.ga));
+        int ti = 0;
+        for (int tile = first; tile < tiles; tile += step, ++ti) {
+            const int tn = GEMV ? tile : tile / p.tiles_m;
+            const int tm = GEMV ? 0 : tile % p.tiles_m;
+            const int as = ti % C::acc_stages;
+            const int n = tn * BM + row;
+            if (!w4::mbar_wait(&afull[as], (uint32_t)(ti / C::acc_stages) & 1u, abort_flag, p.err))
+                break;
+            tc_fence_after();
+            const uint32_t acc = tmem + as * C::acc_cols + ((uint32_t)(quarter * 32) << 16);
+            if constexpr (GEMV) {
+                // two tokens per 16 columns: y = sum_j 8^-j D[8 t + j]
+#pragma unroll 1
+                for (int c = 0; c < BN; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(acc + c, r);
+                    tmem_wait16(r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = c / 8 + h;
+                        float v = __uint_as_float(r[8 * h + 7]);
+#pragma unroll
+                        for (int j = 6; j >= 0; --j)
+                            v = fmaf(v, 0.125f, __uint_as_float(r[8 * h + j]));
+                        if (t < p.M) {
+                            if constexpr (FMT == W4_F4_NV) v *= __ldg(p.row_factor + t) * alpha;
+                            if (p.splits > 1)
+                                part[t * BM + row] = v;
+                            else if (n < p.N)
+                                store_y(p, t, n, v);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 2
+                for (int c = 0; c < BN; c += 16) {
+                    const int t0 = tm * BN + c;
+                    if (t0 >= p.M) break;
+                    uint32_t r[16];
+                    tmem_ld16(acc + c, r);
+                    tmem_wait16(r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = __uint_as_float(r[i]);
+                        if (p.splits > 1)
+                            part[(c + i) * BM + row] = v;
+                        else if (t0 + i < p.M && n < p.N)
+                            store_y(p, t0 + i, n, v * alpha);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) w4::mbar_arrive(&aempty[as]);
+        }
+    }
+
+    if (p.splits > 1) {
+        // one tile per cluster: the partial tiles, summed in CTA order; the
+        // columns are dealt out to the CTAs
+        cluster_sync();
+        if (warp >= kEpiWarp0 && !*abort_flag) {
+            const int row = (warp & 3) * 32 + lane;
+            const int tn = GEMV ? first : first / p.tiles_m;
+            const int t0 = GEMV ? 0 : first % p.tiles_m * BN;
+            const int n = tn * BM + row;
+            const int cols = p.M - t0 < BN ? p.M - t0 : BN;
+            float alpha = 1.0f;
+            if constexpr (FMT == W4_F4_NV && !GEMV) alpha = __fmul_rn(__ldg(p.gw), __ldg(p.ga));
+            const uint32_t base = w4::smem_u32(smem);
+            for (int c = split; c < cols; c += p.splits) {
+                float v[kMaxSplit];
+#pragma unroll
+                for (int q = 0; q < kMaxSplit; ++q)
+                    v[q] = q < p.splits ? ld_cluster(base + (c * BM + row) * 4, q) : 0.0f;
+                float sum = v[0];
+#pragma unroll
+                for (int q = 1; q < kMaxSplit; ++q) sum += v[q];
+                if (n < p.N) store_y(p, t0 + c, n, sum * alpha);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another reads its shared memory
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(C::tmem_cols)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// activation digits of f4_gemv
+// ---------------------------------------------------------------------------
+
+constexpr int kDigitThreads = 256;
+constexpr int kDigitElems = kDigitThreads * 8;  // k of one block of threads
+
+// bf16 magnitude: exponent field, at least 1 (subnormals share the exponent of
+// the smallest normal number).
+__device__ __forceinline__ int exp_field(uint32_t h) {
+    const int e = (int)((h >> 7) & 0xFFu);
+    return e > 0 ? e : 1;
+}
+
+// Token t = blockIdx.y, 8 consecutive k a thread.  With E = floor(log2 amax) of
+// the block, v = x * 2^(21 - E) rounded to an integer has |v| < 2^22, and
+//   v = sum_j d_j 8^(7-j),  d_j in -4..3,  from the base-8 digits of
+//   v + 4 (8^8 - 1) / 7 (each digit shifted by 4),
+// so x = 2^E sum_j d_j 8^-j: digit row 8 t + j, block scale 2^E.
+// NV: e4m3 scales span 2^-9..2^8, so E is taken relative to the token's largest
+// exponent and the rest, 2^(Emax - 8), is the token's factor in the epilogue.
+template <int FMT>
+__global__ void __launch_bounds__(kDigitThreads)
+    digits_kernel(const uint16_t* __restrict__ x, int K, uint8_t* __restrict__ codes,
+                  uint8_t* __restrict__ scales, float* __restrict__ row_factor, int* err) {
+    // the product may start now: it reads only weights before it waits for this
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kBlkLanes = f4::block_of(FMT) / 8;
+    constexpr int kWordLanes = 4 * kBlkLanes;
+    const int t = blockIdx.y;
+    const int lane = threadIdx.x & 31;
+    const uint16_t* xt = x + (int64_t)t * K;
+
+    int emax = 0;  // NV: largest exponent field of the token
+    if constexpr (FMT == W4_F4_NV) {
+        __shared__ uint32_t part[kDigitThreads / 32];
+        uint32_t m = 0;
+        for (int k = threadIdx.x * 8; k < K; k += kDigitElems) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(xt + k));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+        m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
+        if (lane == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kDigitThreads / 32; ++i) m = max(m, part[i]);
+        emax = exp_field(m);
+        // 2^(emax - 127 - 8), as a product where the power itself is subnormal
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            row_factor[t] = __uint_as_float((uint32_t)emax << 23) * 0x1p-8f;
+    }
+
+    const int64_t tiles_k = f4::scale_tiles_k(K, FMT);
+    const int kpad = (int)tiles_k * 4 * f4::block_of(FMT);
+    // whole warps run or skip: kpad is a multiple of 64 k, a warp's span 256,
+    // so the lanes past kpad only take part in the shuffles
+    const int k = blockIdx.x * kDigitElems + threadIdx.x * 8;
+    if (k - lane * 8 >= kpad) return;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (k < K && W4_CHECK(k + 8 <= K, err)) raw = __ldg(reinterpret_cast<const uint4*>(xt + k));
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+    uint32_t amax = max(m2 >> 16, m2 & 0xFFFFu);
+#pragma unroll
+    for (int off = 1; off < kBlkLanes; off <<= 1)
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const bool bad = amax >= 0x7F80u;  // a NaN or an infinity: the scale becomes NaN
+    int eb = exp_field(amax);
+    uint32_t byte;
+    if constexpr (FMT == W4_F4_MX) {
+        byte = bad ? 255u : (uint32_t)eb;
+    } else {
+        if (eb < emax - 17) eb = emax - 17;  // the smallest scale, 2^-9
+        const int s = eb - emax + 8;         // -9..8
+        byte = bad ? 127u : (uint32_t)(s >= -6 ? (s + 7) << 3 : 1 << (s + 9));
+    }
+
+    uint32_t out[kDigits] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+        const int e = exp_field(h);
+        const uint32_t mant = (h & 0x7Fu) | ((h & 0x7F80u) ? 0x80u : 0u);
+        // x = +-mant * 2^(e - 134); v = x * 2^(21 - E) = +-mant * 2^(14 - (eb - e))
+        const int right = eb - e - 14;
+        uint32_t v = right <= 0 ? mant << -right
+                                : (right < 10 ? (mant + (1u << (right - 1))) >> right : 0u);
+        if (bad) v = 0u;
+        const uint32_t u = (h & 0x8000u ? 0u - v : v) + 9586980u;  // 4 (8^8 - 1) / 7
+#pragma unroll
+        for (int j = 0; j < kDigits; ++j) {
+            // e2m1 codes of -4 -3 -2 -1 0 1 2 3, four bits each
+            const uint32_t d = (u >> (3 * (7 - j))) & 7u;
+            out[j] |= ((0x5420ACDEu >> (4 * d)) & 15u) << (4 * i);
+        }
+    }
+    uint32_t word = k < K ? byte << (8 * (lane / kBlkLanes % 4)) : 0u;
+#pragma unroll
+    for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
+        word |= __shfl_xor_sync(0xffffffffu, word, off);
+    if (k < K) {
+#pragma unroll
+        for (int j = 0; j < kDigits; ++j)
+            *reinterpret_cast<uint32_t*>(codes + ((int64_t)(t * kDigits + j) * K + k) / 2) = out[j];
+    }
+    if (lane % kWordLanes == 0 && k < kpad) {
+#pragma unroll
+        for (int j = 0; j < kDigits; ++j)
+            *reinterpret_cast<uint32_t*>(
+                scales + f4::scale_word(t * kDigits + j, k / (4 * f4::block_of(FMT)), tiles_k)) =
+                word;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+// Codes [rows][K/2] in boxes of 128 bytes x box_rows, 128B-swizzled; what lies
+// past the last row or column reads as zero codes.
+bool make_map(CUtensorMap* map, const void* codes, int64_t K, int64_t rows, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kRowBytes, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// CTAs along K for each tile: as many as bring all CTAs onto the GPU at once
+// (`slots` of them), each with at least two stages.
+int choose_splits(int64_t tiles, int stages_k, int slots) {
+    int s = 1;
+    while (s < kMaxSplit && tiles * (s + 1) <= slots && stages_k / (s + 1) >= 2) ++s;
+    return s;
+}
+
+template <int FMT, int BN, bool GEMV>
+int launch_tile(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStream_t stream) {
+    using C = Cfg<FMT, BN>;
+    p.tiles_n = (p.N + BM - 1) / BM;
+    p.tiles_m = (p.b_rows + BN - 1) / BN;
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
+    if (tiles > INT32_MAX / kMaxSplit) return W4_ERR_SHAPE;
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, codes, p.K, p.N, BM) || !make_map(&mb, bcodes, p.K, p.b_rows, BN))
+        return W4_ERR_CUDA;
+    auto kernel = f4_mm_kernel<FMT, BN, GEMV>;
+    static thread_local int attr_dev = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return w4::cuda_fail(e);
+    if (attr_dev != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::total);
+        if (e != cudaSuccess) return w4::cuda_fail(e);
+        attr_dev = dev;
+    }
+    const int per_sm = C::total <= kSmemTwo && C::tmem_cols <= 256 ? 2 : 1;
+    const int slots = w4::sm_count() * per_sm;
+    p.splits = BN <= 128 ? choose_splits(tiles, p.stages_k, slots) : 1;
+    const int64_t grid = p.splits > 1 ? tiles * p.splits : (tiles < slots ? tiles : slots);
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::total;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+    if (e != cudaSuccess) return w4::cuda_fail(e);
+    return w4::launch_status();
+}
+
+template <int FMT>
+int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStream_t st) {
+    // tiles narrower than a 128-row scale tile hold all tokens, so that every
+    // tile starts on a scale tile
+    if (p.M <= 16) return launch_tile<FMT, 16, false>(codes, qa, p, st);
+    if (p.M <= 32) return launch_tile<FMT, 32, false>(codes, qa, p, st);
+    if (p.M <= 64) return launch_tile<FMT, 64, false>(codes, qa, p, st);
+    if (p.M <= 256) return launch_tile<FMT, 128, false>(codes, qa, p, st);
+    return launch_tile<FMT, 256, false>(codes, qa, p, st);
+}
+
+template <int FMT>
+int launch_gemv(const uint8_t* codes, const uint8_t* digits, const Params& p, cudaStream_t st) {
+    if (p.M <= 2) return launch_tile<FMT, 16, true>(codes, digits, p, st);
+    if (p.M <= 4) return launch_tile<FMT, 32, true>(codes, digits, p, st);
+    return launch_tile<FMT, 64, true>(codes, digits, p, st);
+}
+
+bool bad_scalar(const float* g) { return (reinterpret_cast<uintptr_t>(g) & 3u) != 0; }
+
+int fill(Params& p, const uint8_t* scales, const float* g, int64_t N, int64_t K, int format,
+         int64_t M, void* y, int out_dtype) {
+    p = Params{};
+    p.err = w4::device_error_word();
+    if (!p.err) return W4_ERR_CUDA;
+    p.sa = scales;
+    p.gw = g;
+    p.y = y;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.stages_k = (int)((K + BK - 1) / BK);
+    p.tiles_k = (int)f4::scale_tiles_k(K, format);
+    p.out_f32 = out_dtype == W4_OUT_F32;
+    return W4_OK;
+}
+
+// f4_gemv's workspace: digit codes, their scale tiles, a factor for each token.
+struct GemvWs {
+    size_t scales, factors, total;
+};
+GemvWs gemv_ws(int64_t M, int64_t K, int format) {
+    GemvWs w;
+    w.scales = (size_t)(M * kDigits * K / 2 + 511) / 512 * 512;
+    w.factors = w.scales + (size_t)f4::scale_tiles_k(K, format) * f4::kTileBytes;
+    w.total = w.factors + kMaxTokens * sizeof(float);
+    return w;
+}
+
+constexpr int64_t kMaxGemvK = 65536;
+
+bool gemv_range(int64_t M, int64_t N, int64_t K) {
+    return M >= 1 && M <= kMaxTokens && N >= 1 && N <= f4::kMaxRows && K >= 32 && K % 32 == 0 &&
+           K <= kMaxGemvK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N, int64_t K,
+          int format, const uint8_t* qa, const uint8_t* sa, const float* ga, int64_t M, void* y,
+          int out_dtype, void* stream) {
+    if (M < 1 || N < 1 || K < 32 || K % 32 != 0 || K > f4::kMaxK || M > f4::kMaxRows ||
+        N > f4::kMaxRows || !f4::known_format(format) || !f4::known_out(out_dtype))
+        return W4_ERR_SHAPE;
+    const bool nv = format == W4_F4_NV;
+    if (!codes || !scales || !qa || !sa || !y || (nv && (!g || !ga))) return W4_ERR_NULL;
+    if (!w4::aligned16(codes) || !w4::aligned16(scales) || !w4::aligned16(qa) ||
+        !w4::aligned16(sa) || !w4::aligned16(y) || (nv && (bad_scalar(g) || bad_scalar(ga))))
+        return W4_ERR_ALIGN;
+    int rc = w4::check_device();
+    if (rc != W4_OK) return rc;
+    Params p;
+    rc = fill(p, scales, g, N, K, format, M, y, out_dtype);
+    if (rc != W4_OK) return rc;
+    p.sb = sa;
+    p.ga = ga;
+    p.b_rows = (int)M;
+    return nv ? launch_mm<W4_F4_NV>(codes, qa, p, (cudaStream_t)stream)
+              : launch_mm<W4_F4_MX>(codes, qa, p, (cudaStream_t)stream);
+}
+
+size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format) {
+    if (!gemv_range(M, N, K) || !f4::known_format(format)) return 0;
+    return gemv_ws(M, K, format).total;
+}
+
+int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N, int64_t K,
+            int format, const uint16_t* x_bf16, int M, void* y, int out_dtype, void* workspace,
+            size_t ws_bytes, void* stream) {
+    if (!gemv_range(M, N, K) || !f4::known_format(format) || !f4::known_out(out_dtype))
+        return W4_ERR_SHAPE;
+    const bool nv = format == W4_F4_NV;
+    if (!codes || !scales || !x_bf16 || !y || (nv && !g)) return W4_ERR_NULL;
+    if (!w4::aligned16(codes) || !w4::aligned16(scales) || !w4::aligned16(x_bf16) ||
+        !w4::aligned16(y) || (nv && bad_scalar(g)))
+        return W4_ERR_ALIGN;
+    const GemvWs ws = gemv_ws(M, K, format);
+    if (!workspace || ws_bytes < ws.total) return W4_ERR_WORKSPACE;
+    if (!w4::aligned16(workspace)) return W4_ERR_ALIGN;
+    int rc = w4::check_device();
+    if (rc != W4_OK) return rc;
+    Params p;
+    rc = fill(p, scales, g, N, K, format, M, y, out_dtype);
+    if (rc != W4_OK) return rc;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    float* factors = reinterpret_cast<float*>(base + ws.factors);
+    p.sb = base + ws.scales;
+    p.row_factor = factors;
+    p.b_rows = M * kDigits;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const int kpad = p.tiles_k * 4 * f4::block_of(format);
+    const dim3 grid((unsigned)((kpad + kDigitElems - 1) / kDigitElems), (unsigned)M);
+    if (nv)
+        digits_kernel<W4_F4_NV><<<grid, kDigitThreads, 0, st>>>(x_bf16, (int)K, base, base + ws.scales,
+                                                               factors, p.err);
+    else
+        digits_kernel<W4_F4_MX><<<grid, kDigitThreads, 0, st>>>(x_bf16, (int)K, base, base + ws.scales,
+                                                               factors, p.err);
+    rc = w4::launch_status();
+    if (rc != W4_OK) return rc;
+    return nv ? launch_gemv<W4_F4_NV>(codes, base, p, st) : launch_gemv<W4_F4_MX>(codes, base, p, st);
+}
+
+}  // extern "C"
