@@ -425,60 +425,102 @@ def _in_code(x, name: str) -> int:
     torch = _torch()
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    codes = {torch.bfloat16: W4_IN_BF16, torch.float32: W4_IN_F32, torch.float16: W4_IN_F16}
-    if x.dtype not in codes:
-        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
-    return codes[x.dtype]
+    dtype = x.dtype
+    if dtype is torch.bfloat16:
+        return W4_IN_BF16
+    if dtype is torch.float32:
+        return W4_IN_F32
+    if dtype is torch.float16:
+        return W4_IN_F16
+    raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
 
 
-def _stream_on(stream, like):
-    """The stream the call runs on: the caller's, which must belong to the
-    tensors' device, or the current one."""
+# The small calls of these operators take a few microseconds on the GPU, so the
+# checks have a short path for arguments that are right; whatever fails it goes
+# through _need and _on_device, which say what is wrong.
+
+def _is(t, dtype, shape) -> bool:
+    """A plain contiguous tensor of this dtype and shape."""
+    return (type(t) is _torch().Tensor and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous())
+
+
+def _need2d(t, dtype, name: str):
+    """_need for a matrix of any extents."""
+    if not (type(t) is _torch().Tensor and t.dtype is dtype and t.dim() == 2
+            and t.is_contiguous()):
+        _need(t, dtype, name, (None, None))
+
+
+def _run_on(stream, names, *tensors):
+    """Check that all tensors (None: absent) are on the current device; the
+    stream of the call as (torch stream or None for the current one, handle)."""
     torch = _torch()
+    here = tensors[0].get_device()  # -1 on the CPU
+    ok = here >= 0 and here == torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            ok = False
+    if not ok:
+        _on_device(**{n: t for n, t in zip(names, tensors) if t is not None})
     if stream is None:
-        return torch.cuda.current_stream()
-    if stream.device != like.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
-    return stream
+        # the handle behind torch.cuda.current_stream(), without building the object
+        return None, torch._C._cuda_getCurrentRawStream(here)
+    if stream.device != tensors[0].device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {tensors[0].device}")
+    return stream, stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
     """An uninitialised tensor that belongs to the stream the call runs on: the
     allocator then hands its memory out again only in that stream's order."""
     torch = _torch()
-    if stream == torch.cuda.current_stream():
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _f4_scale_shape(R, K: int, format: int):
-    """Shape of the scale plane (row tiles, tiles along K, bytes); an extent
-    that does not follow from the arguments is open."""
-    tiles = -(-K // (4 * F4_BLOCK[format])) if K % 32 == 0 else None
-    return (None if R is None else -(-R // 128), tiles, 512)
+def _f4_scale_shape(R: int, K: int, format: int):
+    """Shape of the scale plane: row tiles, tiles along K, bytes of a tile (the
+    extent along K is open when K breaks the format)."""
+    return (-(-R // 128), -(-K // (4 * F4_BLOCK[format])) if K % 32 == 0 else None, 512)
 
 
 def _f4_planes(codes, scales, g, names, K=None):
     """Check the planes of one 4-bit matrix; returns rows, K, format."""
     torch = _torch()
     cn, sn, gn = names
-    _need(codes, torch.uint8, cn, (None, None if K is None else _div(K, 2)))
-    R, K = codes.shape[0], codes.shape[1] * 2 if K is None else K
+    _need2d(codes, torch.uint8, cn)
+    R, half = codes.shape
+    if K is None:
+        K = 2 * half
+    elif 2 * half != K:
+        _need(codes, torch.uint8, cn, (None, _div(K, 2)))
     format = W4_F4_MX if g is None else W4_F4_NV
-    _need(scales, torch.uint8, sn, _f4_scale_shape(R, K, format))
-    if g is not None:
+    shape = _f4_scale_shape(R, K, format)
+    if not _is(scales, torch.uint8, shape):
+        _need(scales, torch.uint8, sn, shape)
+    if g is not None and not _is(g, torch.float32, (1,)):
         _need(g, torch.float32, gn, (1,))
     return R, K, format
 
 
-def _placed(**tensors):
-    """_on_device for those arguments that are present."""
-    _on_device(**{k: t for k, t in tensors.items() if t is not None})
+def _f4_out(out_dtype, y, M: int, N: int):
+    """Output code and dtype; the caller's y checked against [M,N]."""
+    torch = _torch()
+    if out_dtype is torch.bfloat16 or (out_dtype is None and y is None):
+        oc, dtype = W4_OUT_BF16, torch.bfloat16
+    else:
+        oc = _out_code(out_dtype, y)
+        dtype = torch.float32 if oc == W4_OUT_F32 else torch.bfloat16
+    if y is not None and not _is(y, dtype, (M, N)):
+        _need(y, dtype, "y", (M, N))
+    return oc, dtype
 
 
 def _opt(t):
-    return None if t is None else _ptr(t)
+    return None if t is None else t.data_ptr()
 
 
 def f4_tensor_scale(x, g=None, stream=None):
@@ -486,14 +528,13 @@ def f4_tensor_scale(x, g=None, stream=None):
     elements of x[R,K] (bf16, fp16 or fp32), as an fp32 tensor [1]."""
     torch = _torch()
     ic = _in_code(x, "x")
-    _need(x, x.dtype, "x", (None, None))
+    _need2d(x, x.dtype, "x")
     if g is not None:
         _need(g, torch.float32, "g", (1,))
-    _placed(x=x, g=g)
-    st = _stream_on(stream, x)
+    st, handle = _run_on(stream, ("x", "g"), x, g)
     if g is None:
         g = _new((1,), torch.float32, x, st)
-    _check(load().f4_tensor_scale(_ptr(x), ic, x.shape[0], x.shape[1], _ptr(g), _stream(st)),
+    _check(load().f4_tensor_scale(x.data_ptr(), ic, x.shape[0], x.shape[1], g.data_ptr(), handle),
            "f4_tensor_scale")
     return g
 
@@ -506,51 +547,43 @@ def f4_quantize(x, format="mx", tensor_scale=None, codes=None, scales=None, stre
     omitted)."""
     torch = _torch()
     fc, ic = _f4_format(format), _in_code(x, "x")
-    _need(x, x.dtype, "x", (None, None))
+    _need2d(x, x.dtype, "x")
     R, K = x.shape
-    if tensor_scale is not None:
+    g = tensor_scale
+    if g is not None:
         if fc == W4_F4_MX:
             raise ValueError("tensor_scale belongs to the nv format")
-        _need(tensor_scale, torch.float32, "tensor_scale", (1,))
+        if not _is(g, torch.float32, (1,)):
+            _need(g, torch.float32, "tensor_scale", (1,))
     shape = _f4_scale_shape(R, K, fc)
     if codes is not None:
         _need(codes, torch.uint8, "codes", (R, _div(K, 2)))
     if scales is not None:
         _need(scales, torch.uint8, "scales", shape)
-    _placed(x=x, tensor_scale=tensor_scale, codes=codes, scales=scales)
-    st = _stream_on(stream, x)
+    st, handle = _run_on(stream, ("x", "tensor_scale", "codes", "scales"), x, g, codes, scales)
     if codes is None:
         codes = _new((R, K // 2), torch.uint8, x, st)
     if scales is None:
         scales = _new((shape[0], shape[1] or 0, 512), torch.uint8, x, st)
-    g = tensor_scale
     if fc == W4_F4_NV and g is None:
-        g = f4_tensor_scale(x, stream=st)
-    _check(load().f4_quantize(_ptr(x), ic, R, K, fc, _opt(g), _ptr(codes), _ptr(scales),
-                              _stream(st)), "f4_quantize")
+        g = _new((1,), torch.float32, x, st)
+        _check(load().f4_tensor_scale(x.data_ptr(), ic, R, K, g.data_ptr(), handle),
+               "f4_tensor_scale")
+    _check(load().f4_quantize(x.data_ptr(), ic, R, K, fc, _opt(g), codes.data_ptr(),
+                              scales.data_ptr(), handle), "f4_quantize")
     return codes, scales, g
 
 
 def f4_dequantize(codes, scales, g, out_dtype=None, y=None, stream=None):
     """The values y[R,K] that 4-bit planes stand for, bf16 (default) or fp32."""
     R, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
-    oc = _out_code(out_dtype, y)
-    y, st = _f4_output(y, R, K, oc, stream, codes=codes, scales=scales, g=g)
-    _check(load().f4_dequantize(_ptr(codes), _ptr(scales), _opt(g), R, K, fc, _ptr(y), oc,
-                                _stream(st)), "f4_dequantize")
+    oc, dtype = _f4_out(out_dtype, y, R, K)
+    st, handle = _run_on(stream, ("codes", "scales", "g", "y"), codes, scales, g, y)
+    if y is None:
+        y = _new((R, K), dtype, codes, st)
+    _check(load().f4_dequantize(codes.data_ptr(), scales.data_ptr(), _opt(g), R, K, fc,
+                                y.data_ptr(), oc, handle), "f4_dequantize")
     return y
-
-
-def _f4_output(y, M: int, N: int, oc: int, stream, **placed):
-    """The caller's y checked, or a new one on the call's stream; the stream."""
-    torch = _torch()
-    dtype = torch.float32 if oc == W4_OUT_F32 else torch.bfloat16
-    if y is not None:
-        _need(y, dtype, "y", (M, N))
-    _placed(y=y, **placed)
-    like = next(t for t in placed.values() if t is not None)
-    st = _stream_on(stream, like)
-    return (_new((M, N), dtype, like, st) if y is None else y), st
 
 
 def f4_embed(codes, scales, g, ids, scale=1.0, out_dtype=None, y=None, stream=None):
@@ -558,12 +591,16 @@ def f4_embed(codes, scales, g, ids, scale=1.0, out_dtype=None, y=None, stream=No
     ids int64[T]; an id outside the table (padding) gives a row of zeros."""
     torch = _torch()
     V, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
-    _need(ids, torch.int64, "ids", (None,))
+    if not (type(ids) is torch.Tensor and ids.dtype is torch.int64 and ids.dim() == 1
+            and ids.is_contiguous()):
+        _need(ids, torch.int64, "ids", (None,))
     T = ids.shape[0]
-    oc = _out_code(out_dtype, y)
-    y, st = _f4_output(y, T, K, oc, stream, codes=codes, scales=scales, g=g, ids=ids)
-    _check(load().f4_embed(_ptr(codes), _ptr(scales), _opt(g), V, K, fc, _ptr(ids), T,
-                           float(scale), _ptr(y), oc, _stream(st)), "f4_embed")
+    oc, dtype = _f4_out(out_dtype, y, T, K)
+    st, handle = _run_on(stream, ("codes", "scales", "g", "ids", "y"), codes, scales, g, ids, y)
+    if y is None:
+        y = _new((T, K), dtype, codes, st)
+    _check(load().f4_embed(codes.data_ptr(), scales.data_ptr(), _opt(g), V, K, fc, ids.data_ptr(),
+                           T, float(scale), y.data_ptr(), oc, handle), "f4_embed")
     return y
 
 
@@ -575,10 +612,13 @@ def f4_mm(codes, scales, g, qa, sa, ga, out_dtype=None, y=None, stream=None):
     if (g is None) != (ga is None):
         raise ValueError("g and ga must both be given (nv) or both be None (mx)")
     M, _, _ = _f4_planes(qa, sa, ga, ("qa", "sa", "ga"), K)
-    oc = _out_code(out_dtype, y)
-    y, st = _f4_output(y, M, N, oc, stream, codes=codes, scales=scales, g=g, qa=qa, sa=sa, ga=ga)
-    _check(load().f4_mm(_ptr(codes), _ptr(scales), _opt(g), N, K, fc, _ptr(qa), _ptr(sa),
-                        _opt(ga), M, _ptr(y), oc, _stream(st)), "f4_mm")
+    oc, dtype = _f4_out(out_dtype, y, M, N)
+    st, handle = _run_on(stream, ("codes", "scales", "g", "qa", "sa", "ga", "y"),
+                         codes, scales, g, qa, sa, ga, y)
+    if y is None:
+        y = _new((M, N), dtype, codes, st)
+    _check(load().f4_mm(codes.data_ptr(), scales.data_ptr(), _opt(g), N, K, fc, qa.data_ptr(),
+                        sa.data_ptr(), _opt(ga), M, y.data_ptr(), oc, handle), "f4_mm")
     return y
 
 
@@ -592,16 +632,19 @@ def f4_gemv(codes, scales, g, x, out_dtype=None, y=None, workspace=None, stream=
     tensor of at least f4_gemv_workspace_size(M, N, K, format) bytes (allocated
     here when omitted)."""
     torch = _torch()
-    _need(x, torch.bfloat16, "x", (None, None))
+    _need2d(x, torch.bfloat16, "x")
     M, K = x.shape
     N, _, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"), K)
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace", (None,))
-    oc = _out_code(out_dtype, y)
-    y, st = _f4_output(y, M, N, oc, stream, codes=codes, scales=scales, g=g, x=x,
-                       workspace=workspace)
+    oc, dtype = _f4_out(out_dtype, y, M, N)
+    st, handle = _run_on(stream, ("codes", "scales", "g", "x", "y", "workspace"),
+                         codes, scales, g, x, y, workspace)
+    if y is None:
+        y = _new((M, N), dtype, codes, st)
     if workspace is None:
-        workspace = _new((int(load().f4_gemv_workspace_size(M, N, K, fc)),), torch.uint8, x, st)
-    _check(load().f4_gemv(_ptr(codes), _ptr(scales), _opt(g), N, K, fc, _ptr(x), M, _ptr(y), oc,
-                          _ptr(workspace), workspace.numel(), _stream(st)), "f4_gemv")
+        workspace = _new((load().f4_gemv_workspace_size(M, N, K, fc),), torch.uint8, x, st)
+    _check(load().f4_gemv(codes.data_ptr(), scales.data_ptr(), _opt(g), N, K, fc, x.data_ptr(), M,
+                          y.data_ptr(), oc, workspace.data_ptr(), workspace.numel(), handle),
+           "f4_gemv")
     return y
