@@ -25,7 +25,7 @@ BUILD_DEBUG = os.path.join(BUILD, "debug")
 LIB = os.path.join(PKG, "libw4.so")
 LIB_DEBUG = os.path.join(PKG, "libw4_debug.so")
 SOURCES = ["abi.cu", "pack.cu", "quant.cu", "gemv.cu", "gemv_blockdots.cu", "mmq.cu",
-           "f4_quant.cu", "f4_mm.cu"]
+           "f4_quant.cu", "f4_mm.cu", "f4_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 # No --use_fast_math / -ftz=true / -prec-div=false: the W4A8 product's epilogue
 # multiplies exact integer products held as fp32 denormals, which a
