@@ -18,6 +18,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLaneElems = 8;
 constexpr int kWarpElems = 32 * kLaneElems;  // 256 consecutive k
+constexpr int kSegs = 4;  // segments of a row that a warp has in flight
 
 // ---------------------------------------------------------------------------
 // loads and stores of 8 elements
@@ -67,17 +68,33 @@ __device__ __forceinline__ void widen8(const Raw8<IN>& r, float (&v)[8]) {
     }
 }
 
-// Bits of the largest magnitude of 8 values: for non-negative floats the
-// integer order of the bits is the numeric order, with infinity and then NaN
-// on top.
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[8]) {
-    uint32_t m = 0;
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Largest magnitude of 8 elements in the order of their own bits: for
+// non-negative floats the integer order of the bits is the numeric order, with
+// infinity and then NaN on top.  The 16-bit types go two at a time.
+template <int IN>
+__device__ __forceinline__ uint32_t amax_raw(const Raw8<IN>& r) {
+    if constexpr (IN == W4_IN_F32) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
+        for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+        return m;
+    } else {
+        const uint32_t m = __vmaxu2(__vmaxu2(r.a.x & 0x7FFF7FFFu, r.a.y & 0x7FFF7FFFu),
+                                    __vmaxu2(r.a.z & 0x7FFF7FFFu, r.a.w & 0x7FFF7FFFu));
+        return max(m >> 16, m & 0xFFFFu);
+    }
 }
 
-constexpr uint32_t kInfBits = 0x7F800000u;
+// That magnitude as fp32 bits.
+template <int IN>
+__device__ __forceinline__ uint32_t amax_f32(uint32_t m) {
+    if constexpr (IN == W4_IN_F32) return m;
+    if constexpr (IN == W4_IN_BF16) return m << 16;
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+}
 
 // Eight fp32 values -> eight e2m1 codes (nearest even, saturating), element i
 // in bits 4i..4i+3.
@@ -94,41 +111,15 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     return r;
 }
 
-// Eight e2m1 codes -> fp32.
-__device__ __forceinline__ void from_e2m1x8(uint32_t c, float (&v)[8]) {
-    uint32_t h[4];
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}\n"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(c));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
-template <int OUT>
-__device__ __forceinline__ void store8(void* y, int64_t elem, const float (&v)[8]) {
-    if constexpr (OUT == W4_OUT_F32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(y) + elem);
-        d[0] = make_float4(v[0], v[1], v[2], v[3]);
-        d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + elem) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-    }
+// Two e2m1 codes (low 8 bits) -> fp32.  An e2m1 number has the layout of fp16's
+// top bits, sign, exponent, one mantissa bit, with the exponent 14 lower
+// (subnormals included): the bits moved there are the number times 2^-14.
+__device__ __forceinline__ void from_e2m1x2(uint32_t c, float* v) {
+    const uint32_t w = (c & 0xFu) | ((c & 0xF0u) << 12);
+    const uint32_t h = ((w & 0x00080008u) << 12) | ((w & 0x00070007u) << 9);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    v[0] = f.x * 16384.0f;
+    v[1] = f.y * 16384.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -160,12 +151,17 @@ __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const void* __re
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            float v[8];
-            widen8<IN>(r[u], v);
+            const uint32_t a = amax_f32<IN>(amax_raw<IN>(r[u]));
+            if (a < kInfBits) {
+                m = max(m, a);
+            } else {  // a NaN or an infinity among them: the finite ones one by one
+                float v[8];
+                widen8<IN>(r[u], v);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-                m = max(m, b < kInfBits ? b : 0u);
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+                    m = max(m, b < kInfBits ? b : 0u);
+                }
             }
         }
     }
@@ -185,30 +181,39 @@ __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const void* __re
 // ---------------------------------------------------------------------------
 
 // Scale byte of a block and the factor that its elements are multiplied by.
+// NV (g6 = 6 g, rcp = 1 / g6): the byte is that of the IEEE quotient amax / g6.
+// amax * rcp lies within 2^-22 of it; where e4m3 rounds that product less and
+// plus 2^-21 to one number, the quotient rounds to it too, and only else is the
+// division made (one conversion instruction does both roundings).
 template <int FMT>
-__device__ __forceinline__ void block_scale(uint32_t amax, float g, uint32_t& byte, float& inv) {
-    if (amax >= kInfBits) {  // a NaN or an infinity in the block: codes 0, scale NaN
-        byte = FMT == W4_F4_MX ? 255u : 127u;
-        inv = 0.0f;
-    } else if constexpr (FMT == W4_F4_MX) {
+__device__ __forceinline__ void block_scale(uint32_t amax, float g, float g6, float rcp,
+                                            uint32_t& byte, float& inv) {
+    if constexpr (FMT == W4_F4_MX) {
         // floor(log2(amax)) - 2 from the exponent field; fields 0..2 take 2^-127
         const uint32_t e = amax >> 23;
         byte = e > 2u ? e - 2u : 0u;
         inv = __uint_as_float((254u - byte) << 23);
     } else {
-        const float t = __fdiv_rn(__uint_as_float(amax), __fmul_rn(6.0f, g));
-        byte = __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+        const float q = __uint_as_float(amax) * rcp;
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q * (1.0f - 0x1p-21f),
+                                                                  q * (1.0f + 0x1p-21f)),
+                                                      __NV_SATFINITE, __NV_E4M3);
+        byte = two & 0xFFu;
+        if (byte != two >> 8)
+            byte = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax), g6), __NV_SATFINITE,
+                                         __NV_E4M3);
         const float den = __fmul_rn(f4::scale_value<W4_F4_NV>(byte), g);
         inv = den == 0.0f ? 0.0f : __frcp_rn(den);
     }
+    if (amax >= kInfBits) byte = FMT == W4_F4_MX ? 255u : 127u;  // a NaN or an infinity
 }
 
-// One warp takes 256 consecutive k of one row at a time.  blockIdx.y walks the
-// row's segments, blockIdx.x and the warp the rows, those that only pad the
-// last scale tile among them.
+// A warp takes up to kSegs segments of 256 consecutive k of one row, all loads
+// before the first use.  blockIdx.x and the warp select the row, those that only
+// pad the last scale tile among them, blockIdx.y the segments.
 template <int FMT, int IN>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restrict__ x, int64_t R,
-                                                            int64_t K,
+                                                            int K,
                                                             const float* __restrict__ gp,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales,
@@ -217,41 +222,50 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
     constexpr int kBlkLanes = f4::block_of(FMT) / kLaneElems;  // lanes of a block
     constexpr int kWordLanes = 4 * kBlkLanes;                  // lanes of a scale word
     const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int tiles_k = (int)f4::scale_tiles_k(K, FMT);
+    const int kpad = tiles_k * 4 * f4::block_of(FMT);
+    const int k0 = blockIdx.y * (kSegs * kWarpElems) + lane * kLaneElems;
+    const bool row = r < R;
+    Raw8<IN> raw[kSegs];
+#pragma unroll
+    for (int u = 0; u < kSegs; ++u) {
+        const int k = k0 + u * kWarpElems;
+        raw[u] = Raw8<IN>{};
+        if (row && k < K && W4_CHECK(k + kLaneElems <= K, err)) raw[u] = load8<IN>(x, r * K + k);
+    }
     const float g = FMT == W4_F4_NV ? __ldg(gp) : 1.0f;
-    const int64_t tiles_k = f4::scale_tiles_k(K, FMT);
-    const int64_t rows = f4::row_tiles(R) * f4::kRowTile;
-    const int64_t kpad = tiles_k * 4 * f4::block_of(FMT);
-    for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows;
-         r += (int64_t)gridDim.x * kWarps) {
-        for (int64_t k0 = (int64_t)blockIdx.y * kWarpElems; k0 < kpad;
-             k0 += (int64_t)gridDim.y * kWarpElems) {
-            const int64_t k = k0 + lane * kLaneElems;
-            const bool live = r < R && k < K;  // the same for all lanes of a block
-            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (live && W4_CHECK(k + kLaneElems <= K, err)) widen8<IN>(load8<IN>(x, r * K + k), v);
-            uint32_t amax = amax_bits(v);
+    const float g6 = __fmul_rn(6.0f, g), rcp = __frcp_rn(g6);
+    uint8_t* code_row = codes + r * (K / 2);
+    uint8_t* scale_row = scales + f4::scale_word(r, 0, tiles_k);
 #pragma unroll
-            for (int off = 1; off < kBlkLanes; off <<= 1)
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            uint32_t byte;
-            float inv;
-            block_scale<FMT>(amax, g, byte, inv);
-            const bool bad = amax >= kInfBits;
+    for (int u = 0; u < kSegs; ++u) {
+        const int k = k0 + u * kWarpElems;
+        if (k - lane * kLaneElems >= kpad) break;  // the same for the whole warp
+        const bool live = row && k < K;  // the same for all lanes of a block
+        uint32_t m = amax_raw<IN>(raw[u]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = bad ? 0.0f : __fmul_rn(v[i], inv);
-            const uint32_t c = e2m1x8(v);
-            // the scale bytes of 4 blocks, joined across their lanes
-            uint32_t word = live ? byte << (8 * (lane / kBlkLanes % 4)) : 0u;
+        for (int off = 1; off < kBlkLanes; off <<= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const uint32_t amax = amax_f32<IN>(m);
+        uint32_t byte;
+        float inv;
+        block_scale<FMT>(amax, g, g6, rcp, byte, inv);
+        float v[8];
+        widen8<IN>(raw[u], v);
 #pragma unroll
-            for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
-                word |= __shfl_xor_sync(0xffffffffu, word, off);
-            if (live) *reinterpret_cast<uint32_t*>(codes + (r * K + k) / 2) = c;
-            if (lane % kWordLanes == 0 && k < kpad) {
-                const int64_t at = f4::scale_word(r, k / (4 * f4::block_of(FMT)), tiles_k);
-                if (W4_CHECK(at + 4 <= f4::row_tiles(R) * tiles_k * f4::kTileBytes, err))
-                    *reinterpret_cast<uint32_t*>(scales + at) = word;
-            }
-        }
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], inv);
+        const uint32_t c = amax >= kInfBits ? 0u : e2m1x8(v);
+        // the scale bytes of 4 blocks, joined across their lanes
+        uint32_t word = live ? byte << (8 * (lane / kBlkLanes % 4)) : 0u;
+#pragma unroll
+        for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
+            word |= __shfl_xor_sync(0xffffffffu, word, off);
+        if (live) *reinterpret_cast<uint32_t*>(code_row + k / 2) = c;
+        if (lane % kWordLanes == 0 && k < kpad &&
+            W4_CHECK(r < f4::row_tiles(R) * f4::kRowTile, err))
+            *reinterpret_cast<uint32_t*>(scale_row + k / (4 * f4::block_of(FMT)) * f4::kTileBytes) =
+                word;
     }
 }
 
@@ -259,36 +273,64 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
 // dequantiser and embedding lookup
 // ---------------------------------------------------------------------------
 
-// Output row t is table row ids[t] (or t, without ids) times `alpha` and g.
-// A task is 256 consecutive k of one output row, one per warp and step.
+// Output row t is table row ids[t] (or t, without ids) times `alpha` and g.  A
+// lane owns 16 bytes of output, so that a warp's stores are contiguous; a warp
+// takes up to kSegs segments of one row, all loads before the first use.
 template <int FMT, int OUT, bool LOOKUP>
 __global__ void __launch_bounds__(kThreads)
     rows_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                const float* __restrict__ gp, int64_t V, int64_t K,
+                const float* __restrict__ gp, int64_t V, int K,
                 const int64_t* __restrict__ ids, int64_t T, float alpha, void* __restrict__ y,
                 int* err) {
+    constexpr int kElems = OUT == W4_OUT_F32 ? 4 : 8;  // of a lane
+    constexpr int kSpan = 32 * kElems;                 // of a warp
     const int lane = threadIdx.x & 31;
-    const float c = FMT == W4_F4_NV ? __fmul_rn(__ldg(gp), alpha) : alpha;
-    const int64_t tiles_k = f4::scale_tiles_k(K, FMT);
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < T;
-         t += (int64_t)gridDim.x * kWarps) {
-        const int64_t row = LOOKUP ? __ldg(ids + t) : t;
-        const bool live = row >= 0 && row < V;
-        for (int64_t k0 = (int64_t)blockIdx.y * kWarpElems; k0 < K;
-             k0 += (int64_t)gridDim.y * kWarpElems) {
-            const int64_t k = k0 + lane * kLaneElems;
-            if (k >= K || !W4_CHECK(k + kLaneElems <= K && t < T, err)) continue;
-            float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-            if (live) {
-                const int64_t b = k / f4::block_of(FMT);
-                const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(codes + (row * K + k) / 2));
-                const float s = f4::scale_value<FMT>(
-                    __ldg(scales + f4::scale_word(row, b >> 2, tiles_k) + (b & 3)));
-                from_e2m1x8(q, v);
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const int64_t row = LOOKUP ? __ldg(ids + t) : t;
+    const bool live = row >= 0 && row < V;
+    const uint8_t* code_row = codes + row * (K / 2);
+    const uint8_t* scale_row = scales + f4::scale_word(row, 0, f4::scale_tiles_k(K, FMT));
+    const int k0 = blockIdx.y * (kSegs * kSpan) + lane * kElems;
+    uint32_t q[kSegs], sb[kSegs];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], s), c);
+    for (int u = 0; u < kSegs; ++u) {
+        const int k = k0 + u * kSpan;
+        q[u] = sb[u] = 0u;
+        if (live && k < K && W4_CHECK(k + kElems <= K, err)) {
+            const uint8_t* c = code_row + k / 2;
+            if constexpr (kElems == 8)
+                q[u] = __ldg(reinterpret_cast<const uint32_t*>(c));
+            else
+                q[u] = __ldg(reinterpret_cast<const uint16_t*>(c));
+            const int b = k / f4::block_of(FMT);
+            sb[u] = __ldg(scale_row + (b >> 2) * f4::kTileBytes + (b & 3));
+        }
+    }
+    const float c = FMT == W4_F4_NV ? __fmul_rn(__ldg(gp), alpha) : alpha;
+#pragma unroll
+    for (int u = 0; u < kSegs; ++u) {
+        const int k = k0 + u * kSpan;
+        if (k >= K) break;
+        float v[kElems];
+#pragma unroll
+        for (int i = 0; i < kElems; i += 2) from_e2m1x2(q[u] >> (4 * i), v + i);
+        const float s = f4::scale_value<FMT>(sb[u]);
+#pragma unroll
+        for (int i = 0; i < kElems; ++i)
+            v[i] = live ? __fmul_rn(__fmul_rn(v[i], s), c) : 0.0f;
+        if constexpr (OUT == W4_OUT_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(y) + t * K + k) =
+                make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            store8<OUT>(y, t * K + k, v);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + t * K + k) =
+                make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -301,15 +343,10 @@ bool shape_ok(int64_t R, int64_t K) {
     return R >= 0 && R <= f4::kMaxRows && K >= 0 && K <= f4::kMaxK && K % 32 == 0;
 }
 
-// Rows over blockIdx.x, a row's 256-element segments over blockIdx.y: about
-// eight CTAs per SM in all, the rows first.
-dim3 grid_for(int64_t rows, int64_t segments) {
-    const int64_t cap = (int64_t)w4::sm_count() * 8;
-    int64_t gx = (rows + kWarps - 1) / kWarps;
-    if (gx > cap) gx = cap;
-    int64_t gy = cap / gx;
-    if (gy > segments) gy = segments;
-    return dim3((unsigned)gx, (unsigned)gy);
+// A warp for each row and kSegs spans of `span` elements.
+dim3 grid_for(int64_t rows, int64_t K, int span) {
+    const int64_t per = (int64_t)kSegs * span;
+    return dim3((unsigned)((rows + kWarps - 1) / kWarps), (unsigned)((K + per - 1) / per));
 }
 
 template <int FMT>
@@ -317,28 +354,27 @@ int launch_quantize(const void* x, int in, int64_t R, int64_t K, const float* g,
                     uint8_t* scales, cudaStream_t st) {
     const int64_t rows = f4::row_tiles(R) * f4::kRowTile;
     const int64_t kpad = f4::scale_tiles_k(K, FMT) * 4 * f4::block_of(FMT);
-    const dim3 grid = grid_for(rows, (kpad + kWarpElems - 1) / kWarpElems);
+    const dim3 grid = grid_for(rows, kpad, kWarpElems);
     int* err = w4::device_error_word();
     if (in == W4_IN_BF16)
-        quantize_kernel<FMT, W4_IN_BF16><<<grid, kThreads, 0, st>>>(x, R, K, g, codes, scales, err);
+        quantize_kernel<FMT, W4_IN_BF16><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
     else if (in == W4_IN_F32)
-        quantize_kernel<FMT, W4_IN_F32><<<grid, kThreads, 0, st>>>(x, R, K, g, codes, scales, err);
+        quantize_kernel<FMT, W4_IN_F32><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
     else
-        quantize_kernel<FMT, W4_IN_F16><<<grid, kThreads, 0, st>>>(x, R, K, g, codes, scales, err);
+        quantize_kernel<FMT, W4_IN_F16><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
     return w4::launch_status();
 }
 
 template <int FMT, bool LOOKUP>
 int launch_rows(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t V, int64_t K,
                 const int64_t* ids, int64_t T, float alpha, void* y, int out, cudaStream_t st) {
-    const dim3 grid = grid_for(T, (K + kWarpElems - 1) / kWarpElems);
     int* err = w4::device_error_word();
     if (out == W4_OUT_F32)
-        rows_kernel<FMT, W4_OUT_F32, LOOKUP>
-            <<<grid, kThreads, 0, st>>>(codes, scales, g, V, K, ids, T, alpha, y, err);
+        rows_kernel<FMT, W4_OUT_F32, LOOKUP><<<grid_for(T, K, 128), kThreads, 0, st>>>(
+            codes, scales, g, V, (int)K, ids, T, alpha, y, err);
     else
-        rows_kernel<FMT, W4_OUT_BF16, LOOKUP>
-            <<<grid, kThreads, 0, st>>>(codes, scales, g, V, K, ids, T, alpha, y, err);
+        rows_kernel<FMT, W4_OUT_BF16, LOOKUP><<<grid_for(T, K, 256), kThreads, 0, st>>>(
+            codes, scales, g, V, (int)K, ids, T, alpha, y, err);
     return w4::launch_status();
 }
 
