@@ -340,7 +340,9 @@ int f4_mm(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N
           int64_t K, int format, const uint8_t *qa, const uint8_t *sa,
           const float *ga, int64_t M, void *y, int out_dtype, void *stream);
 
-/* Bytes of device workspace that f4_gemv needs; 0 for sizes outside its range. */
+/* Bytes of device workspace that f4_gemv needs (0 for up to 3 tokens
+ * of MX and 2 of NV, whose digits never leave the kernel, and for sizes outside
+ * its range). */
 size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format);
 
 /* Decode GEMV: y[t][n] = g * sum_k (q * s)[n][k] * x[t][k] with bf16
@@ -349,12 +351,12 @@ size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format);
  * magnitude (every element above 2^-14 of it exact), split into eight base-8
  * digits that are e2m1 numbers, so that the block-scaled tensor cores multiply
  * the weights as they are stored.  (NV: a block below 2^-17 of the token's
- * largest magnitude is held at that block size.)  Accumulated in fp32.
+ * largest magnitude is held as if it were of that size.)  Accumulated in fp32.
  * 1 <= M <= 8, 1 <= N <= 2^24, 32 <= K <= 65536, K % 32 == 0; y: [M][N] of
  * out_dtype.  `workspace` (16-byte aligned) must hold f4_gemv_workspace_size
- * bytes, else W4_ERR_WORKSPACE; it holds the digits, and calls that can
- * overlap on the GPU need one each.  A token with a NaN or an infinity gives
- * NaN outputs. */
+ * bytes, else W4_ERR_WORKSPACE (NULL where that is 0); it holds the digits, and
+ * calls that can overlap on the GPU need one each.  A token with a NaN or an
+ * infinity gives NaN outputs. */
 int f4_gemv(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N,
             int64_t K, int format, const uint16_t *x_bf16, int M, void *y,
             int out_dtype, void *workspace, size_t ws_bytes, void *stream);

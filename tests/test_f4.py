@@ -460,9 +460,9 @@ def test_weights_written_just_before(torch, w4):
 
 def test_workspace_too_small_is_refused(torch, w4):
     w = random_matrix(torch, 64, 96, "mx", 81)
-    x = dev(torch, activations(2, 96, 82)).bfloat16()
-    need = w4.f4_gemv_workspace_size(2, 64, 96, "mx")
-    y = torch.full((2, 64), 9.0, device="cuda")
+    x = dev(torch, activations(5, 96, 82)).bfloat16()
+    need = w4.f4_gemv_workspace_size(5, 64, 96, "mx")
+    y = torch.full((5, 64), 9.0, device="cuda")
     with pytest.raises(w4.W4Error, match="W4_ERR_WORKSPACE"):
         w4.f4_gemv(*w.planes, x, y=y,
                    workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))

@@ -642,9 +642,13 @@ def f4_gemv(codes, scales, g, x, out_dtype=None, y=None, workspace=None, stream=
                          codes, scales, g, x, y, workspace)
     if y is None:
         y = _new((M, N), dtype, codes, st)
-    if workspace is None:
-        workspace = _new((load().f4_gemv_workspace_size(M, N, K, fc),), torch.uint8, x, st)
+    ws_bytes = 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+    elif M > 1:  # a single token never needs any
+        ws_bytes = load().f4_gemv_workspace_size(M, N, K, fc)
+        if ws_bytes:
+            workspace = _new((ws_bytes,), torch.uint8, x, st)
     _check(load().f4_gemv(codes.data_ptr(), scales.data_ptr(), _opt(g), N, K, fc, x.data_ptr(), M,
-                          y.data_ptr(), oc, workspace.data_ptr(), workspace.numel(), handle),
-           "f4_gemv")
+                          y.data_ptr(), oc, _opt(workspace), ws_bytes, handle), "f4_gemv")
     return y

@@ -38,43 +38,55 @@ namespace {
 using namespace f4;
 
 constexpr int BM = 128;   // weight rows of a tile
-constexpr int kThreads = 192;
 constexpr int kEpiWarp0 = 2;
-constexpr int kEpiThreads = 128;
+constexpr int kEpiWarps = 4;
+constexpr int kDigitWarp0 = kEpiWarp0 + kEpiWarps;  // fused f4_gemv: more warps
 constexpr int kDigits = 8;      // base-8 digits of an activation
 constexpr int kMaxTokens = 8;   // f4_gemv
-constexpr int kMaxSplit = 8;    // CTAs of a cluster that share a tile's K
+constexpr int kFusedTokens = 3; // most tokens whose digits the product kernel makes itself
+
+// Tokens up to which f4_gemv is one kernel.  Against digits made by a kernel of
+// their own (us, MX at 1 / 3 / 4 tokens): 2560 x 4096 4.6 / 5.5 / 5.9 against
+// 6.4 / 6.8 / 6.8, 19456 x 2560 7.0 / 9.4 / 10.8 against 9.1 / 9.3 / 9.3,
+// 151936 x 2560 33 / 34.6 / 39.7 against 34.6 / 35.8 / 35.9.  NV looks for the
+// largest exponent first: at 3 tokens 19456 x 2560 takes 12.3 against 10.0.
+constexpr int fused_tokens(int fmt) { return fmt == W4_F4_MX ? 3 : 2; }
+constexpr int kMaxSplit = 6;    // CTAs of a cluster that share a tile's K
 constexpr size_t kSmemTwo = 113 * 1024;  // of each of two CTAs on an SM (228 KB, 1 KB reserved a CTA)
 
-// Everything that depends on the format and the tile's tokens.
+// What a kernel computes.
+enum Mode {
+    kMm,          // f4_mm: the token operand is a 4-bit matrix
+    kGemvPlanes,  // f4_gemv: it is digit rows that the preceding kernel wrote
+    kGemvFused    // f4_gemv: the kernel makes the digits itself
+};
+
 template <int FMT, int BN>
 struct Cfg {
     static constexpr int chunks = BK / (4 * f4::block_of(FMT));  // scale tiles of a stage
     static constexpr int mma_per_chunk = 4 / chunks;             // 2 (MX) or 1 (NV)
-    static constexpr int b_row_tiles = (BN + 127) / 128;
     static constexpr int a_bytes = BM * kRowBytes;
     static constexpr int b_bytes = BN * kRowBytes;
     static constexpr int sa_bytes = chunks * f4::kTileBytes;
-    static constexpr int sb_bytes = b_row_tiles * chunks * f4::kTileBytes;
+    static constexpr int sb_bytes = chunks * f4::kTileBytes;
     static constexpr int stage_bytes = a_bytes + b_bytes + sa_bytes + sb_bytes;
-    // small tiles leave room for a second CTA on the SM
-    static constexpr int stages = BN == 64 ? (FMT == W4_F4_MX ? 4 : 3) : BN == 128 ? 5 : 4;
-    static constexpr int acc_stages = BN <= 128 ? 2 : 1;
-    static constexpr int sf_cols = chunks * 4 * (1 + b_row_tiles);  // TMEM columns per slot
+    // two CTAs run on an SM, so that one streams while the other starts or ends
+    static constexpr int stages = BN == 64 && FMT == W4_F4_NV ? 3 : 4;
+    static constexpr int acc_stages = 2;
+    static constexpr int sf_cols = chunks * 4 * 2;  // TMEM columns per slot
     static constexpr int sf_slots = 2;
     static constexpr int used_cols = acc_stages * (BN < 32 ? 32 : BN) + sf_slots * sf_cols;
-    static constexpr int tmem_cols =
-        used_cols <= 64 ? 64 : used_cols <= 128 ? 128 : used_cols <= 256 ? 256 : 512;
+    static constexpr int tmem_cols = used_cols <= 128 ? 128 : 256;
     static constexpr int acc_cols = BN < 32 ? 32 : BN;
     static constexpr int nbars = 2 * stages + 2 * acc_stages + 1;
     static constexpr int bars = stages * stage_bytes;
-    static constexpr int misc = bars + nbars * 8;
-    static constexpr size_t total = (size_t)misc + 16 + 1024;
-    static_assert(used_cols <= 512, "TMEM has 512 columns");
+    static constexpr int misc = bars + nbars * 8;      // TMEM base, abort flag
+    static constexpr int amax = misc + 16;             // fused f4_gemv: [warps][tokens] maxima
+    static constexpr size_t total = (size_t)amax + 8 * kFusedTokens * 4 + 1024;
+    static_assert(used_cols <= 256, "TMEM has 512 columns, for two CTAs");
     static_assert(stage_bytes % 1024 == 0, "operand tiles start on swizzle atoms");
-    static_assert(total <= kSmemMax, "shared memory of one CTA");
-    static_assert((size_t)BN * BM * 4 <= (size_t)stages * stage_bytes || BN > 128,
-                  "a partial tile fits the ring");
+    static_assert(total <= kSmemTwo, "shared memory of an SM, for two CTAs");
+    static_assert((size_t)BN * BM * 4 <= (size_t)stages * stage_bytes, "a partial tile fits the ring");
 };
 
 struct Params {
@@ -82,10 +94,11 @@ struct Params {
     const uint8_t* sb;  // token scales
     const float* gw;    // NV: tensor scales (token: f4_mm only)
     const float* ga;
-    const float* row_factor;  // f4_gemv: factor of each token
+    const float* row_factor;  // f4_gemv with digit planes: factor of each token
+    const uint16_t* x;        // fused f4_gemv: activations
     void* y;
     int M, N;          // tokens, weight rows
-    int b_rows;        // rows of the token operand
+    int b_rows;        // rows of the token operand (f4_gemv: 8 M)
     int K;
     int stages_k;      // ceil(K / BK)
     int tiles_k;       // scale tiles along K
@@ -104,17 +117,152 @@ __device__ __forceinline__ void store_y(const Params& p, int64_t t, int n, float
         static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
 }
 
+// Four consecutive weight rows of token t.
+__device__ __forceinline__ void store_y4(const Params& p, int64_t t, int n, float4 v, float alpha) {
+    const float f[4] = {v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha};
+    if (p.N % 4 == 0 && n < p.N) {  // y's rows start on 4 elements: one vector
+        if (!W4_CHECK(t >= 0 && t < p.M && n >= 0 && n + 4 <= p.N, p.err)) return;
+        const int64_t at = t * p.N + n;
+        if (p.out_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) =
+                make_float4(f[0], f[1], f[2], f[3]);
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2], f[3]);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                           *reinterpret_cast<const uint32_t*>(&hi));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) store_y(p, t, n + i, f[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// activation digits of f4_gemv
+// ---------------------------------------------------------------------------
+//
+// With E = floor(log2 amax) of a block, v = x * 2^(21 - E) rounded to an integer
+// has |v| < 2^22, and
+//   v = sum_j d_j 8^(7-j),  d_j in -4..3,  from the base-8 digits of
+//   v + 4 (8^8 - 1) / 7 (each digit shifted by 4),
+// so x = 2^E sum_j d_j 8^-j: digit rows 8 t + j of token t with block scale 2^E.
+// NV: e4m3 scales span 2^-9..2^8, so E is taken relative to the largest exponent
+// Emax among the k that one accumulation sees, and the rest, 2^(Emax - 8), is a
+// factor in the epilogue.
+
+// bf16 magnitude: exponent field, at least 1 (subnormals share the exponent of
+// the smallest normal number).
+__device__ __forceinline__ int exp_field(uint32_t h) {
+    const int e = (int)((h >> 7) & 0xFFu);
+    return e > 0 ? e : 1;
+}
+
+// Largest magnitude (15 bits) of 8 bf16 numbers.
+__device__ __forceinline__ uint32_t amax8(const uint4& v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return max(m >> 16, m & 0xFFFFu);
+}
+
+// The factor 2^(emax - 127 - 8) of an exponent field, as a product where the
+// power itself is subnormal.
+__device__ __forceinline__ float nv_factor(int emax) {
+    return __uint_as_float((uint32_t)emax << 23) * 0x1p-8f;
+}
+
+// The 8 digits of each of a lane's 8 elements: out[j] holds digit j's e2m1
+// codes, element i in bits 4i..4i+3; `word` the scale bytes of the 4 blocks that
+// this lane's block shares a scale word with.  All 32 lanes take part; `live` is
+// false past the end of K (zero digits, zero scale).  emax: NV only.
+template <int FMT>
+__device__ __forceinline__ void digits8(const uint4& raw, bool live, int emax, int lane,
+                                        uint32_t (&out)[kDigits], uint32_t& word) {
+    constexpr int kBlkLanes = block_of(FMT) / 8;
+    constexpr int kWordLanes = 4 * kBlkLanes;
+    uint32_t amax = amax8(raw);
+#pragma unroll
+    for (int off = 1; off < kBlkLanes; off <<= 1)
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const bool bad = amax >= 0x7F80u;  // a NaN or an infinity: the scale becomes NaN
+    int eb = exp_field(amax);
+    uint32_t byte;
+    if constexpr (FMT == W4_F4_MX) {
+        byte = bad ? 255u : (uint32_t)eb;
+    } else {
+        if (eb < emax - 17) eb = emax - 17;  // the smallest scale, 2^-9
+        const int s = eb - emax + 8;         // -9..8
+        byte = bad ? 127u : (uint32_t)(s >= -6 ? (s + 7) << 3 : 1 << (s + 9));
+    }
+    word = live ? byte << (8 * (lane / kBlkLanes % 4)) : 0u;
+#pragma unroll
+    for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
+        word |= __shfl_xor_sync(0xffffffffu, word, off);
+
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t lo[4], hi[4];  // codes of digits 7..4 and 3..0, a byte each, by pair of elements
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+        const int e = exp_field(h);
+        const uint32_t mant = (h & 0x7Fu) | ((h & 0x7F80u) ? 0x80u : 0u);
+        // x = +-mant * 2^(e - 134); v = x * 2^(21 - E) = +-mant * 2^(14 - (eb - e)),
+        // rounded half up in magnitude
+        const int right = eb - e - 14;
+        uint32_t v = right <= 0 ? mant << -right
+                                : (right < 10 ? (mant + (1u << (right - 1))) >> right : 0u);
+        if (bad) v = 0u;
+        uint32_t u = (h & 0x8000u ? 0u - v : v) + 9586980u;  // 4 (8^8 - 1) / 7
+        // octal digits to nibbles, then each to its e2m1 code by table
+        u = (u & 0x00000FFFu) | ((u & 0x00FFF000u) << 4);
+        u = (u & 0x003F003Fu) | ((u & 0x0FC00FC0u) << 2);
+        u = (u & 0x07070707u) | ((u & 0x38383838u) << 1);
+        // -4 -3 -2 -1 | 0 1 2 3
+        const uint32_t a = __byte_perm(0x0A0C0D0Eu, 0x05040200u, u);
+        const uint32_t b = __byte_perm(0x0A0C0D0Eu, 0x05040200u, u >> 16);
+        lo[i / 2] = i & 1 ? lo[i / 2] | a << 4 : a;
+        hi[i / 2] = i & 1 ? hi[i / 2] | b << 4 : b;
+    }
+    // byte i of the four pairs -> one word
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t(&p)[4] = q ? hi : lo;
+        const uint32_t t0 = __byte_perm(p[0], p[1], 0x5140), t1 = __byte_perm(p[2], p[3], 0x5140);
+        const uint32_t t2 = __byte_perm(p[0], p[1], 0x7362), t3 = __byte_perm(p[2], p[3], 0x7362);
+        out[7 - 4 * q] = __byte_perm(t0, t1, 0x5410);
+        out[6 - 4 * q] = __byte_perm(t0, t1, 0x7632);
+        out[5 - 4 * q] = __byte_perm(t2, t3, 0x5410);
+        out[4 - 4 * q] = __byte_perm(t2, t3, 0x7632);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // kernel
 // ---------------------------------------------------------------------------
 
-// GEMV: the token operand holds digit rows (8 per token) that the preceding
-// kernel wrote; otherwise one row per token.
-template <int FMT, int BN, bool GEMV>
-__global__ void __launch_bounds__(kThreads)
+// Digit warps of the fused f4_gemv: a warp takes about 1300 cycles for a token's
+// stage, which one SM's share of HBM delivers every 850.
+constexpr int digit_warps(int bn) { return bn / kDigits * 2; }
+
+constexpr int threads_of(int bn, Mode mode) {
+    return 32 * (kDigitWarp0 + (mode == kGemvFused ? digit_warps(bn) : 0));
+}
+
+// Digit and epilogue warps meet: the maxima of the tokens are in shared memory.
+template <int BN>
+__device__ __forceinline__ void digit_barrier() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * (kEpiWarps + digit_warps(BN))) : "memory");
+}
+
+template <int FMT, int BN, Mode MODE>
+__global__ void __launch_bounds__(threads_of(BN, MODE))
     f4_mm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const Params p) {
     using C = Cfg<FMT, BN>;
+    constexpr bool GEMV = MODE != kMm;
+    constexpr bool FUSED = MODE == kGemvFused;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -135,14 +283,18 @@ __global__ void __launch_bounds__(kThreads)
     const int kb = (int)((int64_t)p.stages_k * split / p.splits);
     const int ke = (int)((int64_t)p.stages_k * (split + 1) / p.splits);
 
+    // a following kernel of this library may start; it waits for this one
+    // before it touches global memory
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::stages; ++i) {
-            w4::mbar_init(&full[i], 1);
+            // the producer, and a digit warp for each token
+            w4::mbar_init(&full[i], FUSED ? 1 + p.M : 1);
             w4::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < C::acc_stages; ++i) {
             w4::mbar_init(&afull[i], 1);
-            w4::mbar_init(&aempty[i], kEpiThreads / 32);
+            w4::mbar_init(&aempty[i], kEpiWarps);
         }
         w4::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -164,13 +316,13 @@ __global__ void __launch_bounds__(kThreads)
         // ---------------- TMA producer ----------------
         if (w4::elect_one()) {
             w4::prefetch_tmap(&tm_a);
-            w4::prefetch_tmap(&tm_b);
+            if constexpr (!FUSED) w4::prefetch_tmap(&tm_b);
             const int chunks_last = p.tiles_k - (p.stages_k - 1) * C::chunks;
             auto chunks_of = [&](int ks) { return ks + 1 < p.stages_k ? C::chunks : chunks_last; };
             auto load_a = [&](int s, int ks, int tn) {
                 const int ch = chunks_of(ks);
-                w4::mbar_arrive_expect_tx(
-                    &full[s], C::a_bytes + C::b_bytes + ch * f4::kTileBytes * (1 + C::b_row_tiles));
+                w4::mbar_arrive_expect_tx(&full[s], C::a_bytes + ch * f4::kTileBytes +
+                                                        (FUSED ? 0 : C::b_bytes + ch * f4::kTileBytes));
                 uint8_t* st = smem + s * C::stage_bytes;
                 w4::tma_load_2d(st, &tm_a, &full[s], ks * kRowBytes, tn * BM);
                 w4::bulk_load_1d(st + C::a_bytes + C::b_bytes,
@@ -182,27 +334,20 @@ __global__ void __launch_bounds__(kThreads)
                 const int ch = chunks_of(ks);
                 uint8_t* st = smem + s * C::stage_bytes;
                 w4::tma_load_2d(st + C::a_bytes, &tm_b, &full[s], ks * kRowBytes, tm * BN);
-                // row tiles of the token scales; one past the last reads the last again
-                const int last = (p.b_rows - 1) / f4::kRowTile;
-#pragma unroll
-                for (int rt = 0; rt < C::b_row_tiles; ++rt) {
-                    int tile = tm * C::b_row_tiles + rt;
-                    if (tile > last) tile = last;
-                    w4::bulk_load_1d(st + C::a_bytes + C::b_bytes + C::sa_bytes +
-                                         rt * C::chunks * f4::kTileBytes,
-                                     p.sb + ((int64_t)tile * p.tiles_k + (int64_t)ks * C::chunks) *
-                                                f4::kTileBytes,
-                                     (uint32_t)(ch * f4::kTileBytes), &full[s]);
-                }
+                w4::bulk_load_1d(st + C::a_bytes + C::b_bytes + C::sa_bytes,
+                                 p.sb + ((int64_t)(tm * BN / f4::kRowTile) * p.tiles_k +
+                                         (int64_t)ks * C::chunks) *
+                                            f4::kTileBytes,
+                                 (uint32_t)(ch * f4::kTileBytes), &full[s]);
             };
             int it = 0;  // stages issued
             bool ok = true;
-            // f4_gemv: the weights do not depend on the digit kernel that
-            // precedes this one, so the first stages' are requested before the
-            // wait for it (that kernel starts this one only after everything
-            // before it has completed)
+            // the weights do not depend on the digit kernel that precedes this
+            // one, so the first stages' are requested before the wait for it
+            // (that kernel starts this one only after everything before it has
+            // completed)
             int pre = 0;
-            if constexpr (GEMV) {
+            if constexpr (MODE == kGemvPlanes) {
                 if (first < tiles) pre = ke - kb < C::stages ? ke - kb : C::stages;
                 for (int i = 0; i < pre; ++i) load_a(i, kb + i, first % p.tiles_n);
             }
@@ -221,7 +366,7 @@ __global__ void __launch_bounds__(kThreads)
                         }
                         load_a(s, ks, tn);
                     }
-                    load_b(s, ks, tm);
+                    if constexpr (!FUSED) load_b(s, ks, tm);
                 }
             }
             // drain: every issued load must land before the CTA exits
@@ -235,6 +380,10 @@ __global__ void __launch_bounds__(kThreads)
             int it = 0, ti = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step, ++ti) {
+                // an odd 64-token tile starts in the middle of its 128-row scale
+                // tile, at TMEM column 2 (32 rows a column; scale addresses must
+                // be even, so narrower tiles come one to a product)
+                const uint32_t sb_col = !GEMV && BN == 64 ? (uint32_t)(tile % p.tiles_m & 1) * 2 : 0u;
                 const int as = ti % C::acc_stages;
                 const uint32_t d = tmem + as * C::acc_cols;
                 if (!w4::mbar_wait(&aempty[as], ((uint32_t)(ti / C::acc_stages) & 1u) ^ 1u,
@@ -262,10 +411,7 @@ __global__ void __launch_bounds__(kThreads)
                     for (int c = 0; c < C::chunks; ++c) {
                         if (c * C::mma_per_chunk >= steps) break;
                         copy_scales(sf + c * 4, scale_desc(sa + c * f4::kTileBytes));
-#pragma unroll
-                        for (int rt = 0; rt < C::b_row_tiles; ++rt)
-                            copy_scales(sfb + (c * C::b_row_tiles + rt) * 4,
-                                        scale_desc(sb + (rt * C::chunks + c) * f4::kTileBytes));
+                        copy_scales(sfb + c * 4, scale_desc(sb + c * f4::kTileBytes));
                     }
 #pragma unroll
                     for (int j = 0; j < BK / kMmaK; ++j) {
@@ -274,7 +420,7 @@ __global__ void __launch_bounds__(kThreads)
                         const int id = j % C::mma_per_chunk * 2;
                         mma_f4<FMT>(d, operand_desc(a + j * (kMmaK / 2)),
                                     operand_desc(b + j * (kMmaK / 2)), instr_desc<FMT, BM, BN>(id),
-                                    sf + c * 4, sfb + c * C::b_row_tiles * 4,
+                                    sf + c * 4, sfb + c * 4 + sb_col,
                                     ks > kb || j > 0);
                     }
                     mma_commit(&empty[s]);
@@ -285,6 +431,73 @@ __global__ void __launch_bounds__(kThreads)
             mma_commit(drain);
             w4::mbar_wait(drain, 0u, nullptr, p.err);
         }
+    } else if (FUSED && warp >= kDigitWarp0) {
+        // ---------------- activation digits ----------------
+        // Warp w makes the digits of token w mod M, of every `per`-th stage from
+        // w / M on: 8 rows of 128 bytes of the stage's token operand (one
+        // swizzle atom) and their scale words.
+        constexpr int kDigitWarps = digit_warps(BN);
+        const int w = warp - kDigitWarp0;
+        const int per = kDigitWarps / p.M;  // warps that share a token
+        const int t = w % p.M, turn = w / p.M;
+        constexpr int kWordLanes = block_of(FMT) / 2;
+        pdl_wait();
+        const uint16_t* xt = p.x + (int64_t)t * p.K;
+        const int k_end = ke * BK < p.K ? ke * BK : p.K;
+        int emax = 0;
+        if constexpr (FMT == W4_F4_NV) {
+            // the largest exponent of this CTA's k, over all four warps
+            volatile uint32_t* part = reinterpret_cast<volatile uint32_t*>(smem + C::amax);
+            for (int tt = 0; tt < p.M; ++tt) {
+                uint32_t m = 0;
+                for (int k = kb * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
+                    m = max(m, amax8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)tt * p.K + k))));
+                m = __reduce_max_sync(0xffffffffu, m);
+                if (lane == 0) part[w * kFusedTokens + tt] = m;
+            }
+            digit_barrier<BN>();
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kDigitWarps; ++i) m = max(m, part[i * kFusedTokens + t]);
+            emax = exp_field(m);
+        }
+        // the activations of the warp's next stage are loaded before it works on
+        // the present one; the stages of one tile follow those of the tile before
+        const int stages = ke - kb;
+        const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * stages : 0;
+        auto load_x = [&](int i) {
+            const int k = (kb + i % stages) * BK + lane * 8;
+            if (i < total && k < p.K && W4_CHECK(k + 8 <= p.K && t < p.M, p.err))
+                return __ldg(reinterpret_cast<const uint4*>(xt + k));
+            return make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (turn < per) {  // (three tokens may leave a warp without work)
+            uint4 next = load_x(turn);
+            for (int it = turn; it < total; it += per) {
+                const uint4 raw = next;
+                next = load_x(it + per);
+                const bool live = (kb + it % stages) * BK + lane * 8 < p.K;
+                uint32_t out[kDigits], word;
+                digits8<FMT>(raw, live, emax, lane, out, word);
+                const int s = it % C::stages;
+                if (!w4::mbar_wait(&empty[s], ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort_flag,
+                                   p.err))
+                    break;
+                uint8_t* rows = smem + s * C::stage_bytes + C::a_bytes + t * kDigits * kRowBytes;
+#pragma unroll
+                for (int j = 0; j < kDigits; ++j)
+                    *reinterpret_cast<uint32_t*>(rows + j * kRowBytes + (((lane >> 2) ^ j) << 4) +
+                                                 (lane & 3) * 4) = out[j];
+                // scale rows 8 t .. 8 t + 7 of the word's tile
+                uint8_t* sc = smem + s * C::stage_bytes + C::a_bytes + C::b_bytes + C::sa_bytes +
+                              lane / kWordLanes * kTileBytes + t * kDigits * 16;
+                if (lane % kWordLanes < kDigits)
+                    *reinterpret_cast<uint32_t*>(sc + lane % kWordLanes * 16) = word;
+                w4::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) w4::mbar_arrive(&full[s]);
+            }
+        }
     } else {
         // ---------------- epilogue ----------------
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
@@ -293,6 +506,19 @@ __global__ void __launch_bounds__(kThreads)
         float* part = reinterpret_cast<float*>(smem);  // split K: [column][128] in the ring
         pdl_wait();
         if constexpr (FMT == W4_F4_NV) alpha = GEMV ? __ldg(p.gw) : __fmul_rn(__ldg(p.gw), __ldg(p.ga));
+        if constexpr (FUSED && FMT == W4_F4_NV) digit_barrier<BN>();
+        // NV: the factor that the digits of token t leave out
+        auto factor = [&](int t) {
+            if constexpr (FUSED) {
+                const volatile uint32_t* part = reinterpret_cast<const volatile uint32_t*>(smem + C::amax);
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < digit_warps(BN); ++i) m = max(m, part[i * kFusedTokens + t]);
+                return nv_factor(exp_field(m));
+            } else {
+                return __ldg(p.row_factor + t);
+            }
+        };
         int ti = 0;
         for (int tile = first; tile < tiles; tile += step, ++ti) {
             const int tn = GEMV ? tile : tile / p.tiles_m;
@@ -318,7 +544,7 @@ __global__ void __launch_bounds__(kThreads)
                         for (int j = 6; j >= 0; --j)
                             v = fmaf(v, 0.125f, __uint_as_float(r[8 * h + j]));
                         if (t < p.M) {
-                            if constexpr (FMT == W4_F4_NV) v *= __ldg(p.row_factor + t) * alpha;
+                            if constexpr (FMT == W4_F4_NV) v *= factor(t) * alpha;
                             if (p.splits > 1)
                                 part[t * BM + row] = v;
                             else if (n < p.N)
@@ -354,24 +580,42 @@ __global__ void __launch_bounds__(kThreads)
         // one tile per cluster: the partial tiles, summed in CTA order; the
         // columns are dealt out to the CTAs
         cluster_sync();
-        if (warp >= kEpiWarp0 && !*abort_flag) {
-            const int row = (warp & 3) * 32 + lane;
+        if (warp >= kEpiWarp0 && warp < kDigitWarp0 && !*abort_flag) {
             const int tn = GEMV ? first : first / p.tiles_m;
             const int t0 = GEMV ? 0 : first % p.tiles_m * BN;
-            const int n = tn * BM + row;
+            const int row = lane * 4, n = tn * BM + row;  // four weight rows a thread
             const int cols = p.M - t0 < BN ? p.M - t0 : BN;
             float alpha = 1.0f;
             if constexpr (FMT == W4_F4_NV && !GEMV) alpha = __fmul_rn(__ldg(p.gw), __ldg(p.ga));
-            const uint32_t base = w4::smem_u32(smem);
-            for (int c = split; c < cols; c += p.splits) {
-                float v[kMaxSplit];
+            const uint32_t base = w4::smem_u32(smem) + row * 4;
+            // columns split, split + splits, ...: one a warp and step, two steps'
+            // loads in flight
+            const int cstep = p.splits * (kEpiWarps);
+#pragma unroll 1
+            for (int c = split + p.splits * (warp - kEpiWarp0); c < cols; c += 2 * cstep) {
+                float4 v[2][kMaxSplit];
 #pragma unroll
-                for (int q = 0; q < kMaxSplit; ++q)
-                    v[q] = q < p.splits ? ld_cluster(base + (c * BM + row) * 4, q) : 0.0f;
-                float sum = v[0];
+                for (int u = 0; u < 2; ++u) {
+                    const int cu = c + u * cstep;
 #pragma unroll
-                for (int q = 1; q < kMaxSplit; ++q) sum += v[q];
-                if (n < p.N) store_y(p, t0 + c, n, sum * alpha);
+                    for (int q = 0; q < kMaxSplit; ++q)
+                        v[u][q] = q < p.splits && cu < cols ? ld_cluster(base + cu * BM * 4, q)
+                                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int cu = c + u * cstep;
+                    if (cu >= cols) break;
+                    float4 sum = v[u][0];
+#pragma unroll
+                    for (int q = 1; q < kMaxSplit; ++q) {
+                        sum.x += v[u][q].x;
+                        sum.y += v[u][q].y;
+                        sum.z += v[u][q].z;
+                        sum.w += v[u][q].w;
+                    }
+                    store_y4(p, t0 + cu, n, sum, alpha);
+                }
             }
         }
         cluster_sync();  // no CTA leaves while another reads its shared memory
@@ -387,34 +631,20 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------
-// activation digits of f4_gemv
+// f4_gemv of more tokens than fused_tokens: the digits in global memory
 // ---------------------------------------------------------------------------
 
 constexpr int kDigitThreads = 256;
 constexpr int kDigitElems = kDigitThreads * 8;  // k of one block of threads
 
-// bf16 magnitude: exponent field, at least 1 (subnormals share the exponent of
-// the smallest normal number).
-__device__ __forceinline__ int exp_field(uint32_t h) {
-    const int e = (int)((h >> 7) & 0xFFu);
-    return e > 0 ? e : 1;
-}
-
-// Token t = blockIdx.y, 8 consecutive k a thread.  With E = floor(log2 amax) of
-// the block, v = x * 2^(21 - E) rounded to an integer has |v| < 2^22, and
-//   v = sum_j d_j 8^(7-j),  d_j in -4..3,  from the base-8 digits of
-//   v + 4 (8^8 - 1) / 7 (each digit shifted by 4),
-// so x = 2^E sum_j d_j 8^-j: digit row 8 t + j, block scale 2^E.
-// NV: e4m3 scales span 2^-9..2^8, so E is taken relative to the token's largest
-// exponent and the rest, 2^(Emax - 8), is the token's factor in the epilogue.
+// Token t = blockIdx.y, 8 consecutive k a thread.
 template <int FMT>
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const uint16_t* __restrict__ x, int K, uint8_t* __restrict__ codes,
                   uint8_t* __restrict__ scales, float* __restrict__ row_factor, int* err) {
     // the product may start now: it reads only weights before it waits for this
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kBlkLanes = f4::block_of(FMT) / 8;
-    constexpr int kWordLanes = 4 * kBlkLanes;
+    constexpr int kWordLanes = block_of(FMT) / 2;
     const int t = blockIdx.y;
     const int lane = threadIdx.x & 31;
     const uint16_t* xt = x + (int64_t)t * K;
@@ -423,73 +653,29 @@ __global__ void __launch_bounds__(kDigitThreads)
     if constexpr (FMT == W4_F4_NV) {
         __shared__ uint32_t part[kDigitThreads / 32];
         uint32_t m = 0;
-        for (int k = threadIdx.x * 8; k < K; k += kDigitElems) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(xt + k));
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-        }
-        m = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
+        for (int k = threadIdx.x * 8; k < K; k += kDigitElems)
+            m = max(m, amax8(__ldg(reinterpret_cast<const uint4*>(xt + k))));
+        m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kDigitThreads / 32; ++i) m = max(m, part[i]);
         emax = exp_field(m);
-        // 2^(emax - 127 - 8), as a product where the power itself is subnormal
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            row_factor[t] = __uint_as_float((uint32_t)emax << 23) * 0x1p-8f;
+        if (blockIdx.x == 0 && threadIdx.x == 0) row_factor[t] = nv_factor(emax);
     }
 
-    const int64_t tiles_k = f4::scale_tiles_k(K, FMT);
-    const int kpad = (int)tiles_k * 4 * f4::block_of(FMT);
-    // whole warps run or skip: kpad is a multiple of 64 k, a warp's span 256,
-    // so the lanes past kpad only take part in the shuffles
+    const int64_t tiles_k = scale_tiles_k(K, FMT);
+    const int kpad = (int)tiles_k * 4 * block_of(FMT);
+    // whole warps run or skip; in a warp that runs, the lanes past kpad only
+    // take part in the shuffles
     const int k = blockIdx.x * kDigitElems + threadIdx.x * 8;
     if (k - lane * 8 >= kpad) return;
+    const bool live = k < K;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (k < K && W4_CHECK(k + 8 <= K, err)) raw = __ldg(reinterpret_cast<const uint4*>(xt + k));
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t m2 = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
-    uint32_t amax = max(m2 >> 16, m2 & 0xFFFFu);
-#pragma unroll
-    for (int off = 1; off < kBlkLanes; off <<= 1)
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    const bool bad = amax >= 0x7F80u;  // a NaN or an infinity: the scale becomes NaN
-    int eb = exp_field(amax);
-    uint32_t byte;
-    if constexpr (FMT == W4_F4_MX) {
-        byte = bad ? 255u : (uint32_t)eb;
-    } else {
-        if (eb < emax - 17) eb = emax - 17;  // the smallest scale, 2^-9
-        const int s = eb - emax + 8;         // -9..8
-        byte = bad ? 127u : (uint32_t)(s >= -6 ? (s + 7) << 3 : 1 << (s + 9));
-    }
-
-    uint32_t out[kDigits] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t h = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-        const int e = exp_field(h);
-        const uint32_t mant = (h & 0x7Fu) | ((h & 0x7F80u) ? 0x80u : 0u);
-        // x = +-mant * 2^(e - 134); v = x * 2^(21 - E) = +-mant * 2^(14 - (eb - e))
-        const int right = eb - e - 14;
-        uint32_t v = right <= 0 ? mant << -right
-                                : (right < 10 ? (mant + (1u << (right - 1))) >> right : 0u);
-        if (bad) v = 0u;
-        const uint32_t u = (h & 0x8000u ? 0u - v : v) + 9586980u;  // 4 (8^8 - 1) / 7
-#pragma unroll
-        for (int j = 0; j < kDigits; ++j) {
-            // e2m1 codes of -4 -3 -2 -1 0 1 2 3, four bits each
-            const uint32_t d = (u >> (3 * (7 - j))) & 7u;
-            out[j] |= ((0x5420ACDEu >> (4 * d)) & 15u) << (4 * i);
-        }
-    }
-    uint32_t word = k < K ? byte << (8 * (lane / kBlkLanes % 4)) : 0u;
-#pragma unroll
-    for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
-        word |= __shfl_xor_sync(0xffffffffu, word, off);
-    if (k < K) {
+    if (live && W4_CHECK(k + 8 <= K, err)) raw = __ldg(reinterpret_cast<const uint4*>(xt + k));
+    uint32_t out[kDigits], word;
+    digits8<FMT>(raw, live, emax, lane, out, word);
+    if (live) {
 #pragma unroll
         for (int j = 0; j < kDigits; ++j)
             *reinterpret_cast<uint32_t*>(codes + ((int64_t)(t * kDigits + j) * K + k) / 2) = out[j];
@@ -498,8 +684,7 @@ __global__ void __launch_bounds__(kDigitThreads)
 #pragma unroll
         for (int j = 0; j < kDigits; ++j)
             *reinterpret_cast<uint32_t*>(
-                scales + f4::scale_word(t * kDigits + j, k / (4 * f4::block_of(FMT)), tiles_k)) =
-                word;
+                scales + scale_word(t * kDigits + j, k / (4 * block_of(FMT)), tiles_k)) = word;
     }
 }
 
@@ -507,53 +692,65 @@ __global__ void __launch_bounds__(kDigitThreads)
 // host
 // ---------------------------------------------------------------------------
 
-// CTAs along K for each tile: as many as bring all CTAs onto the GPU at once
-// (`slots` of them), each with at least two stages.
-int choose_splits(int64_t tiles, int stages_k, int slots) {
-    int s = 1;
-    while (s < kMaxSplit && tiles * (s + 1) <= slots && stages_k / (s + 1) >= 2) ++s;
-    return s;
-}
-
-template <int FMT, int BN, bool GEMV>
-int launch_tile(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStream_t stream) {
+template <int FMT, int BN, Mode MODE>
+int launch_tiles(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStream_t stream) {
     using C = Cfg<FMT, BN>;
     p.tiles_n = (p.N + BM - 1) / BM;
     p.tiles_m = (p.b_rows + BN - 1) / BN;
     const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
-    if (tiles > INT32_MAX / kMaxSplit) return W4_ERR_SHAPE;
     CUtensorMap ma, mb;
-    if (!make_map(&ma, codes, p.K, p.N, BM) || !make_map(&mb, bcodes, p.K, p.b_rows, BN))
+    if (!make_map(&ma, codes, p.K, p.N, BM)) return W4_ERR_CUDA;
+    if (MODE == kGemvFused)
+        mb = ma;  // not read
+    else if (!make_map(&mb, bcodes, p.K, p.b_rows, BN))
         return W4_ERR_CUDA;
-    auto kernel = f4_mm_kernel<FMT, BN, GEMV>;
-    static thread_local int attr_dev = -1;
+    auto kernel = f4_mm_kernel<FMT, BN, MODE>;
+    // of the device: whether the shared-memory limit is raised, and how many
+    // clusters of each size run at once (0: not asked yet)
+    static thread_local int dev_of = -1;
+    static thread_local int clusters[kMaxSplit + 1];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return w4::cuda_fail(e);
-    if (attr_dev != dev) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)C::total);
+    if (dev_of != dev) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
         if (e != cudaSuccess) return w4::cuda_fail(e);
-        attr_dev = dev;
+        for (int& c : clusters) c = 0;
+        dev_of = dev;
     }
-    const int per_sm = C::total <= kSmemTwo && C::tmem_cols <= 256 ? 2 : 1;
-    const int slots = w4::sm_count() * per_sm;
-    p.splits = BN <= 128 ? choose_splits(tiles, p.stages_k, slots) : 1;
-    const int64_t grid = p.splits > 1 ? tiles * p.splits : (tiles < slots ? tiles : slots);
-
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(BN, MODE));
     cfg.dynamicSmemBytes = C::total;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    // CTAs along K of each tile: as many as still run all at once, with at
+    // least two stages each
+    p.splits = 1;
+    for (int s = kMaxSplit; s > 1; --s) {
+        if (p.stages_k / s < 2 || tiles * s > 2 * (int64_t)w4::sm_count()) continue;
+        if (clusters[s] == 0) {
+            attr[0].val.clusterDim.x = (unsigned)s;
+            cfg.gridDim = dim3((unsigned)s);
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&clusters[s], kernel, &cfg);
+            if (e != cudaSuccess) return w4::cuda_fail(e);
+            if (clusters[s] == 0) clusters[s] = -1;
+        }
+        if (tiles <= clusters[s]) {
+            p.splits = s;
+            break;
+        }
+    }
+    const int64_t slots = (int64_t)w4::sm_count() * 2;
+    const int64_t grid = p.splits > 1 ? tiles * p.splits : (tiles < slots ? tiles : slots);
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
     if (e != cudaSuccess) return w4::cuda_fail(e);
@@ -563,19 +760,23 @@ int launch_tile(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStrea
 template <int FMT>
 int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStream_t st) {
     // tiles narrower than a 128-row scale tile hold all tokens, so that every
-    // tile starts on a scale tile
-    if (p.M <= 16) return launch_tile<FMT, 16, false>(codes, qa, p, st);
-    if (p.M <= 32) return launch_tile<FMT, 32, false>(codes, qa, p, st);
-    if (p.M <= 64) return launch_tile<FMT, 64, false>(codes, qa, p, st);
-    if (p.M <= 256) return launch_tile<FMT, 128, false>(codes, qa, p, st);
-    return launch_tile<FMT, 256, false>(codes, qa, p, st);
+    // tile starts on one
+    if (p.M <= 16) return launch_tiles<FMT, 16, kMm>(codes, qa, p, st);
+    if (p.M <= 32) return launch_tiles<FMT, 32, kMm>(codes, qa, p, st);
+    return launch_tiles<FMT, 64, kMm>(codes, qa, p, st);
 }
 
 template <int FMT>
-int launch_gemv(const uint8_t* codes, const uint8_t* digits, const Params& p, cudaStream_t st) {
-    if (p.M <= 2) return launch_tile<FMT, 16, true>(codes, digits, p, st);
-    if (p.M <= 4) return launch_tile<FMT, 32, true>(codes, digits, p, st);
-    return launch_tile<FMT, 64, true>(codes, digits, p, st);
+int launch_fused(const uint8_t* codes, const Params& p, cudaStream_t st) {
+    if constexpr (fused_tokens(FMT) > 2)
+        if (p.M > 2) return launch_tiles<FMT, 32, kGemvFused>(codes, nullptr, p, st);
+    return launch_tiles<FMT, 16, kGemvFused>(codes, nullptr, p, st);
+}
+
+template <int FMT>
+int launch_planes(const uint8_t* codes, const uint8_t* digits, const Params& p, cudaStream_t st) {
+    if (p.M <= 4) return launch_tiles<FMT, 32, kGemvPlanes>(codes, digits, p, st);
+    return launch_tiles<FMT, 64, kGemvPlanes>(codes, digits, p, st);
 }
 
 bool bad_scalar(const float* g) { return (reinterpret_cast<uintptr_t>(g) & 3u) != 0; }
@@ -633,7 +834,8 @@ int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N
         return W4_ERR_ALIGN;
     int rc = w4::check_device();
     if (rc != W4_OK) return rc;
-    if (M > 64) {
+    // wide tiles for CTA pairs, unless one round of 128 x 64 tiles covers y
+    if (row_tiles(N) * ((M + 63) / 64) > w4::sm_count() && M > 64) {
         const PairArgs a{codes, scales, g, N, K, qa, sa, ga, M, y, w4::device_error_word()};
         return launch_pair(a, format, out_dtype, (cudaStream_t)stream);
     }
@@ -648,7 +850,9 @@ int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N
 }
 
 size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format) {
-    if (!gemv_range(M, N, K) || !f4::known_format(format)) return 0;
+    if (!gemv_range(M, N, K) || !f4::known_format(format) ||
+        M <= fused_tokens(format))
+        return 0;
     return gemv_ws(M, K, format).total;
 }
 
@@ -662,20 +866,27 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     if (!w4::aligned16(codes) || !w4::aligned16(scales) || !w4::aligned16(x_bf16) ||
         !w4::aligned16(y) || (nv && bad_scalar(g)))
         return W4_ERR_ALIGN;
+    const bool fused = M <= fused_tokens(format);
     const GemvWs ws = gemv_ws(M, K, format);
-    if (!workspace || ws_bytes < ws.total) return W4_ERR_WORKSPACE;
-    if (!w4::aligned16(workspace)) return W4_ERR_ALIGN;
+    if (!fused) {
+        if (!workspace || ws_bytes < ws.total) return W4_ERR_WORKSPACE;
+        if (!w4::aligned16(workspace)) return W4_ERR_ALIGN;
+    }
     int rc = w4::check_device();
     if (rc != W4_OK) return rc;
     Params p;
     rc = fill(p, scales, g, N, K, format, M, y, out_dtype);
     if (rc != W4_OK) return rc;
+    p.b_rows = M * kDigits;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (fused) {
+        p.x = x_bf16;
+        return nv ? launch_fused<W4_F4_NV>(codes, p, st) : launch_fused<W4_F4_MX>(codes, p, st);
+    }
     uint8_t* base = static_cast<uint8_t*>(workspace);
     float* factors = reinterpret_cast<float*>(base + ws.factors);
     p.sb = base + ws.scales;
     p.row_factor = factors;
-    p.b_rows = M * kDigits;
-    const cudaStream_t st = (cudaStream_t)stream;
     const int kpad = p.tiles_k * 4 * f4::block_of(format);
     const dim3 grid((unsigned)((kpad + kDigitElems - 1) / kDigitElems), (unsigned)M);
     if (nv)
@@ -686,7 +897,8 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
                                                                factors, p.err);
     rc = w4::launch_status();
     if (rc != W4_OK) return rc;
-    return nv ? launch_gemv<W4_F4_NV>(codes, base, p, st) : launch_gemv<W4_F4_MX>(codes, base, p, st);
+    return nv ? launch_planes<W4_F4_NV>(codes, base, p, st)
+              : launch_planes<W4_F4_MX>(codes, base, p, st);
 }
 
 }  // extern "C"
