@@ -714,6 +714,10 @@ int launch_tiles(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStre
     if (e != cudaSuccess) return w4::cuda_fail(e);
     if (dev_of != dev) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
+        // all of the SM's memory as shared memory: two CTAs
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return w4::cuda_fail(e);
         for (int& c : clusters) c = 0;
         dev_of = dev;
@@ -740,9 +744,12 @@ int launch_tiles(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStre
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&clusters[s], kernel, &cfg);
             if (e != cudaSuccess) return w4::cuda_fail(e);
-            if (clusters[s] == 0) clusters[s] = -1;
+            if (clusters[s] == 0) clusters[s] = -1;  // asked, none
         }
-        if (tiles <= clusters[s]) {
+        // the query counts one CTA an SM where two run: 48 tiles still start at
+        // once in clusters of 5 (26 by the query) and no longer in 6 (22), 80 in
+        // 3 (45) and not in 4 (33), each step too far costing half as much again
+        if (tiles <= 2 * clusters[s]) {
             p.splits = s;
             break;
         }
