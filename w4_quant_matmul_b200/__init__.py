@@ -457,11 +457,11 @@ def _run_on(stream, names, *tensors):
     stream of the call as (torch stream or None for the current one, handle)."""
     torch = _torch()
     here = tensors[0].get_device()  # -1 on the CPU
-    ok = here >= 0 and here == torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
-            ok = False
-    if not ok:
+            here = -1
+            break
+    if here < 0 or here != torch.cuda.current_device():
         _on_device(**{n: t for n, t in zip(names, tensors) if t is not None})
     if stream is None:
         # the handle behind torch.cuda.current_stream(), without building the object
@@ -490,18 +490,22 @@ def _f4_scale_shape(R: int, K: int, format: int):
 def _f4_planes(codes, scales, g, names, K=None):
     """Check the planes of one 4-bit matrix; returns rows, K, format."""
     torch = _torch()
+    T, u8 = torch.Tensor, torch.uint8
+    format, word = (W4_F4_MX, 128) if g is None else (W4_F4_NV, 64)
+    if (type(codes) is T and codes.dtype is u8 and codes.dim() == 2 and codes.is_contiguous()
+            and type(scales) is T and scales.dtype is u8 and scales.is_contiguous()):
+        R, half = codes.shape
+        k = 2 * half
+        if (k % 32 == 0 and (K is None or K == k)
+                and scales.shape == ((R + 127) // 128, (k + word - 1) // word, 512)
+                and (g is None or _is(g, torch.float32, (1,)))):
+            return R, k, format
     cn, sn, gn = names
-    _need2d(codes, torch.uint8, cn)
-    R, half = codes.shape
-    if K is None:
-        K = 2 * half
-    elif 2 * half != K:
-        _need(codes, torch.uint8, cn, (None, _div(K, 2)))
-    format = W4_F4_MX if g is None else W4_F4_NV
-    shape = _f4_scale_shape(R, K, format)
-    if not _is(scales, torch.uint8, shape):
-        _need(scales, torch.uint8, sn, shape)
-    if g is not None and not _is(g, torch.float32, (1,)):
+    _need(codes, u8, cn, (None, None if K is None else _div(K, 2)))
+    R = codes.shape[0]
+    K = codes.shape[1] * 2 if K is None else K
+    _need(scales, u8, sn, _f4_scale_shape(R, K, format))
+    if g is not None:
         _need(g, torch.float32, gn, (1,))
     return R, K, format
 
