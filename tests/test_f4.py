@@ -410,6 +410,63 @@ def test_captured_and_replayed(torch, w4, fmt):
                 assert torch.equal(t, r)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_plain_calls_are_the_same_calls(torch, w4, fmt):
+    """The extension's calls against the ctypes way, which a caller's y takes;
+    on another current stream too."""
+    from w4_quant_matmul_b200 import _f4call
+    assert w4._calls() is _f4call
+    w, a = random_matrix(torch, 300, 160, fmt, 91), random_matrix(torch, 70, 160, fmt, 92)
+    x = dev(torch, activations(6, 160, 93)).bfloat16()
+    ids = dev(torch, np.array([0, 299, 300, 7]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for out in (None, torch.bfloat16, torch.float32):
+        dt = out or torch.bfloat16
+        new = lambda *s: torch.empty(s, dtype=dt, device="cuda")
+        for here in (torch.cuda.current_stream(), side):
+            with torch.cuda.stream(here):
+                for m in (1, 3, 6):
+                    xm = x[:m].contiguous()
+                    got = w4.f4_gemv(*w.planes, xm, out_dtype=out)
+                    assert got.dtype == dt
+                    assert torch.equal(got, w4.f4_gemv(*w.planes, xm, y=new(m, 300)))
+                assert torch.equal(w4.f4_mm(*w.planes, *a.planes, out_dtype=out),
+                                   w4.f4_mm(*w.planes, *a.planes, y=new(70, 300)))
+                assert torch.equal(w4.f4_embed(*w.planes, ids, 2.5, out_dtype=out),
+                                   w4.f4_embed(*w.planes, ids, 2.5, y=new(4, 160)))
+                assert torch.equal(w4.f4_dequantize(*w.planes, out_dtype=out),
+                                   w4.f4_dequantize(*w.planes, y=new(300, 160)))
+    torch.cuda.synchronize()
+    for src in (x, x.float(), x.half()):
+        c, s, g = w4.f4_quantize(src, fmt)
+        c2, s2, g2 = w4.f4_quantize(src, fmt, codes=torch.empty_like(c))
+        assert torch.equal(c, c2) and torch.equal(s, s2)
+        assert g is None and g2 is None or torch.equal(g, g2)
+        if fmt == "nv":
+            assert w4.f4_quantize(src, fmt, tensor_scale=g)[2] is g
+
+
+def test_wrong_calls_fall_through_to_the_checks(torch, w4):
+    w = random_matrix(torch, 300, 160, "mx", 94)
+    x = dev(torch, activations(2, 160, 95)).bfloat16()
+    with pytest.raises(ValueError, match="^x must be contiguous"):
+        w4.f4_gemv(*w.planes, dev(torch, activations(160, 2, 95)).bfloat16().t())
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        w4.f4_gemv(*w.planes, x.cpu())
+    with pytest.raises(ValueError, match="^codes must have shape"):
+        w4.f4_gemv(*w.planes, x[:, :128].contiguous())
+    with pytest.raises(w4.W4Error, match="W4_ERR_SHAPE"):
+        w4.f4_gemv(*w.planes, x[:0])
+    with pytest.raises(w4.W4Error, match="W4_ERR_SHAPE"):
+        w4.f4_gemv(*w.planes, x[:1].expand(9, 160).contiguous())
+    with pytest.raises(ValueError, match="unsupported out_dtype"):
+        w4.f4_gemv(*w.planes, x, out_dtype=torch.float16)
+    # a parameter is a tensor like any other
+    p = torch.nn.Parameter(x, requires_grad=False)
+    assert torch.equal(w4.f4_gemv(*w.planes, p), w4.f4_gemv(*w.planes, x))
+
+
 def test_outputs_stay_inside(torch, w4):
     # guard bands around the outputs of ragged sizes
     for fmt in FORMATS:

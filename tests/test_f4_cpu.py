@@ -85,6 +85,17 @@ def test_bounds_catch_a_swapped_nibble():
     assert (np.abs(a @ swapped.T - a @ wv.T) > xb).mean() > 0.5
 
 
+def test_the_extension_is_built_and_bound(lib):
+    from w4_quant_matmul_b200 import build
+    import os
+    assert os.path.exists(build.CALLS)
+    from w4_quant_matmul_b200 import _f4call
+    assert w4._calls() is _f4call
+    # without tensors that it can take it leaves the call to the checks
+    assert _f4call.mm(1, 2, None, 3, 4, None, None) is None
+    assert _f4call.gemv(torch.zeros(2, 2), None, None, None, None) is None
+
+
 # ---------------------------------------------------------------------------
 # C ABI
 # ---------------------------------------------------------------------------

@@ -435,9 +435,33 @@ def _in_code(x, name: str) -> int:
     raise TypeError(f"{name} must be bfloat16, float16 or float32, got {dtype}")
 
 
-# The small calls of these operators take a few microseconds on the GPU, so the
-# checks have a short path for arguments that are right; whatever fails it goes
-# through _need and _on_device, which say what is wrong.
+# The small calls of these operators take a few microseconds on the GPU.  Plain
+# calls (no y, workspace or stream of the caller's) with arguments that are right
+# are therefore made by _f4call, an extension that checks, allocates and calls
+# without the interpreter; it returns None for any other call, which then takes
+# the way below: checks with a short path, and _need and _on_device to say what
+# is wrong.  Without the extension every call does.
+_ext = None
+
+
+def _calls():
+    """The extension, bound to the loaded library; False if it is not built."""
+    global _ext
+    if _ext is None:
+        import ctypes
+        torch, lib = _torch(), load()
+        try:
+            from . import _f4call as ext
+        except ImportError:
+            _ext = False
+            return False
+        names = ("f4_tensor_scale", "f4_quantize", "f4_dequantize", "f4_embed", "f4_mm", "f4_gemv",
+                 "f4_gemv_workspace_size")
+        ext.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                 torch.bfloat16, torch.float32)
+        _ext = ext
+    return _ext
+
 
 def _is(t, dtype, shape) -> bool:
     """A plain contiguous tensor of this dtype and shape."""
@@ -550,7 +574,12 @@ def f4_quantize(x, format="mx", tensor_scale=None, codes=None, scales=None, stre
     of 16, e4m3 scales, g fp32[1]: `tensor_scale`, or found from x when
     omitted)."""
     torch = _torch()
-    fc, ic = _f4_format(format), _in_code(x, "x")
+    fc = _f4_format(format)
+    if codes is None and scales is None and stream is None:
+        out = (_ext or _calls()) and _ext.quantize(x, fc, tensor_scale)
+        if out:
+            return out
+    ic = _in_code(x, "x")
     _need2d(x, x.dtype, "x")
     R, K = x.shape
     g = tensor_scale
@@ -580,6 +609,10 @@ def f4_quantize(x, format="mx", tensor_scale=None, codes=None, scales=None, stre
 
 def f4_dequantize(codes, scales, g, out_dtype=None, y=None, stream=None):
     """The values y[R,K] that 4-bit planes stand for, bf16 (default) or fp32."""
+    if y is None and stream is None and (_ext or _calls()):
+        out = _ext.dequantize(codes, scales, g, out_dtype)
+        if out is not None:
+            return out
     R, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
     oc, dtype = _f4_out(out_dtype, y, R, K)
     st, handle = _run_on(stream, ("codes", "scales", "g", "y"), codes, scales, g, y)
@@ -593,6 +626,10 @@ def f4_dequantize(codes, scales, g, out_dtype=None, y=None, stream=None):
 def f4_embed(codes, scales, g, ids, scale=1.0, out_dtype=None, y=None, stream=None):
     """Embedding lookup: y[t] = scale * row ids[t] of the 4-bit table, for
     ids int64[T]; an id outside the table (padding) gives a row of zeros."""
+    if y is None and stream is None and (_ext or _calls()):
+        out = _ext.embed(codes, scales, g, ids, scale, out_dtype)
+        if out is not None:
+            return out
     torch = _torch()
     V, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
     if not (type(ids) is torch.Tensor and ids.dtype is torch.int64 and ids.dim() == 1
@@ -612,6 +649,10 @@ def f4_mm(codes, scales, g, qa, sa, ga, out_dtype=None, y=None, stream=None):
     """y[M,N] = A W^T from 4-bit weight planes (codes, scales, g) of W[N,K] and
     4-bit activation planes (qa, sa, ga) of A[M,K], both of one format
     (f4_quantize), on the block-scaled tensor cores."""
+    if y is None and stream is None and (_ext or _calls()):
+        out = _ext.mm(codes, scales, g, qa, sa, ga, out_dtype)
+        if out is not None:
+            return out
     N, K, fc = _f4_planes(codes, scales, g, ("codes", "scales", "g"))
     if (g is None) != (ga is None):
         raise ValueError("g and ga must both be given (nv) or both be None (mx)")
@@ -635,6 +676,10 @@ def f4_gemv(codes, scales, g, x, out_dtype=None, y=None, workspace=None, stream=
     activations (not quantised to 4 bits).  workspace: optional uint8 1-D device
     tensor of at least f4_gemv_workspace_size(M, N, K, format) bytes (allocated
     here when omitted)."""
+    if y is None and workspace is None and stream is None and (_ext or _calls()):
+        out = _ext.gemv(codes, scales, g, x, out_dtype)
+        if out is not None:
+            return out
     torch = _torch()
     _need2d(x, torch.bfloat16, "x")
     M, K = x.shape

@@ -5,16 +5,21 @@ with the static CUDA runtime so the library is self-contained.
     python -m w4_quant_matmul_b200.build --force  # rebuild everything
     python -m w4_quant_matmul_b200.build --debug  # libw4_debug.so (-DW4_DEBUG)
 
+The release build also compiles ``_f4call.so``, the plain calls of the f4_*
+functions as a Python extension (g++, torch's headers; no kernels in it).
+
 The ptxas resource report (registers, spills, shared memory per kernel) is
 written to ``_build/ptxas.log``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +29,9 @@ BUILD = os.path.join(ROOT, "_build")
 BUILD_DEBUG = os.path.join(BUILD, "debug")
 LIB = os.path.join(PKG, "libw4.so")
 LIB_DEBUG = os.path.join(PKG, "libw4_debug.so")
+# Python extension with the plain calls of the f4_* functions (no kernels)
+CALLS = os.path.join(PKG, "_f4call.so")
+CALLS_SOURCE = "f4call.cpp"
 SOURCES = ["abi.cu", "pack.cu", "quant.cu", "gemv.cu", "gemv_blockdots.cu", "mmq.cu",
            "f4_quant.cu", "f4_mm.cu", "f4_pair.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -72,14 +80,37 @@ def _compile(src: str, force: bool, debug: bool = False) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile ``_f4call.so`` against the installed torch."""
+    src = os.path.join(CSRC, CALLS_SOURCE)
+    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "w4.h")]):
+        return CALLS
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    nvcc = _nvcc()
+    cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
+    include = [INCLUDE, os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC"] + [f"-I{d}" for d in include] + \
+          [src, "-o", CALLS, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Compile every CUDA source for sm_100a and link ``libw4.so`` (with
     ``debug``: the -DW4_DEBUG build with device-side index checks,
     ``libw4_debug.so``)."""
     out_dir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(out_dir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = None if debug else ex.submit(build_calls, force)
         results = list(ex.map(lambda s: _compile(s, force, debug), SOURCES))
+        if calls:
+            calls.result()
     objs = [o for o, _ in results]
     with open(os.path.join(out_dir, "ptxas.log"), "w") as f:
         for src, (_, log) in zip(SOURCES, results):
