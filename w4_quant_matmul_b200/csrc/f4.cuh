@@ -46,6 +46,33 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     }
 }
 
+// Programmatic dependent launch.  Every f4 kernel waits for the kernel before it
+// ahead of its first access to global memory (f4_gemv's product: to anything but
+// weights) and only then lets the kernel after it start, so that a kernel that
+// starts early is one ahead of what has completed, never two.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch that may start while the kernel before it on the stream still runs.
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream,
+                     Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+    if (e != cudaSuccess) return w4::cuda_fail(e);
+    return w4::launch_status();
+}
+
 // Host checks of a format and an out_dtype.
 inline bool known_format(int fmt) { return fmt == W4_F4_MX || fmt == W4_F4_NV; }
 inline bool known_out(int t) { return t == W4_OUT_BF16 || t == W4_OUT_F32; }

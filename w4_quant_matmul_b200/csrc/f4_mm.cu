@@ -283,9 +283,6 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     const int kb = (int)((int64_t)p.stages_k * split / p.splits);
     const int ke = (int)((int64_t)p.stages_k * (split + 1) / p.splits);
 
-    // a following kernel of this library may start; it waits for this one
-    // before it touches global memory
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::stages; ++i) {
             // the producer, and a digit warp for each token
@@ -352,6 +349,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                 for (int i = 0; i < pre; ++i) load_a(i, kb + i, first % p.tiles_n);
             }
             pdl_wait();
+            pdl_trigger();
             for (int tile = first; tile < tiles && ok; tile += step) {
                 const int tn = GEMV ? tile : tile / p.tiles_m;
                 const int tm = GEMV ? 0 : tile % p.tiles_m;
@@ -642,8 +640,10 @@ template <int FMT>
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const uint16_t* __restrict__ x, int K, uint8_t* __restrict__ codes,
                   uint8_t* __restrict__ scales, float* __restrict__ row_factor, int* err) {
-    // the product may start now: it reads only weights before it waits for this
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // after the wait all that came before is complete: the product may start,
+    // and read the weights before it waits for this kernel
+    pdl_wait();
+    pdl_trigger();
     constexpr int kWordLanes = block_of(FMT) / 2;
     const int t = blockIdx.y;
     const int lane = threadIdx.x & 31;
@@ -896,13 +896,8 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     p.row_factor = factors;
     const int kpad = p.tiles_k * 4 * f4::block_of(format);
     const dim3 grid((unsigned)((kpad + kDigitElems - 1) / kDigitElems), (unsigned)M);
-    if (nv)
-        digits_kernel<W4_F4_NV><<<grid, kDigitThreads, 0, st>>>(x_bf16, (int)K, base, base + ws.scales,
-                                                               factors, p.err);
-    else
-        digits_kernel<W4_F4_MX><<<grid, kDigitThreads, 0, st>>>(x_bf16, (int)K, base, base + ws.scales,
-                                                               factors, p.err);
-    rc = w4::launch_status();
+    rc = launch_dependent(nv ? digits_kernel<W4_F4_NV> : digits_kernel<W4_F4_MX>, grid, kDigitThreads,
+                          st, x_bf16, (int)K, base, base + ws.scales, factors, p.err);
     if (rc != W4_OK) return rc;
     return nv ? launch_planes<W4_F4_NV>(codes, base, p, st)
               : launch_planes<W4_F4_MX>(codes, base, p, st);

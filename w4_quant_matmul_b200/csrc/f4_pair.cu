@@ -173,9 +173,6 @@ __global__ void __launch_bounds__(kThreads)
     const int tiles = p.tiles_n * p.tiles_m;
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
-    // a following kernel of this library may start; it waits for this one
-    // before it touches global memory
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::stages; ++i) {
             w4::mbar_init(&full[i], 1);
@@ -210,6 +207,7 @@ __global__ void __launch_bounds__(kThreads)
             w4::prefetch_tmap(&tm_sa);
             w4::prefetch_tmap(&tm_sb);
             pdl_wait();
+            pdl_trigger();
             int it = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {

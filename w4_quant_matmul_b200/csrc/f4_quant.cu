@@ -138,6 +138,8 @@ template <int IN>
 __global__ void __launch_bounds__(kThreads) tensor_scale_kernel(const void* __restrict__ x,
                                                                 int64_t chunks,
                                                                 float* __restrict__ g, int* err) {
+    f4::pdl_wait();
+    f4::pdl_trigger();
     constexpr int kU = 4;
     uint32_t m = 0;
     const int64_t stride = (int64_t)gridDim.x * kThreads;
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales,
                                                             int* err) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    f4::pdl_wait();
+    f4::pdl_trigger();
     constexpr int kBlkLanes = f4::block_of(FMT) / kLaneElems;  // lanes of a block
     constexpr int kWordLanes = 4 * kBlkLanes;                  // lanes of a scale word
     const int lane = threadIdx.x & 31;
@@ -282,6 +285,8 @@ __global__ void __launch_bounds__(kThreads)
                 const float* __restrict__ gp, int64_t V, int K,
                 const int64_t* __restrict__ ids, int64_t T, float alpha, void* __restrict__ y,
                 int* err) {
+    f4::pdl_wait();
+    f4::pdl_trigger();
     constexpr int kElems = OUT == W4_OUT_F32 ? 4 : 8;  // of a lane
     constexpr int kSpan = 32 * kElems;                 // of a warp
     const int lane = threadIdx.x & 31;
@@ -356,26 +361,20 @@ int launch_quantize(const void* x, int in, int64_t R, int64_t K, const float* g,
     const int64_t kpad = f4::scale_tiles_k(K, FMT) * 4 * f4::block_of(FMT);
     const dim3 grid = grid_for(rows, kpad, kWarpElems);
     int* err = w4::device_error_word();
-    if (in == W4_IN_BF16)
-        quantize_kernel<FMT, W4_IN_BF16><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
-    else if (in == W4_IN_F32)
-        quantize_kernel<FMT, W4_IN_F32><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
-    else
-        quantize_kernel<FMT, W4_IN_F16><<<grid, kThreads, 0, st>>>(x, R, (int)K, g, codes, scales, err);
-    return w4::launch_status();
+    auto kernel = in == W4_IN_BF16  ? quantize_kernel<FMT, W4_IN_BF16>
+                  : in == W4_IN_F32 ? quantize_kernel<FMT, W4_IN_F32>
+                                    : quantize_kernel<FMT, W4_IN_F16>;
+    return f4::launch_dependent(kernel, grid, kThreads, st, x, R, (int)K, g, codes, scales, err);
 }
 
 template <int FMT, bool LOOKUP>
 int launch_rows(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t V, int64_t K,
                 const int64_t* ids, int64_t T, float alpha, void* y, int out, cudaStream_t st) {
     int* err = w4::device_error_word();
-    if (out == W4_OUT_F32)
-        rows_kernel<FMT, W4_OUT_F32, LOOKUP><<<grid_for(T, K, 128), kThreads, 0, st>>>(
-            codes, scales, g, V, (int)K, ids, T, alpha, y, err);
-    else
-        rows_kernel<FMT, W4_OUT_BF16, LOOKUP><<<grid_for(T, K, 256), kThreads, 0, st>>>(
-            codes, scales, g, V, (int)K, ids, T, alpha, y, err);
-    return w4::launch_status();
+    const bool f32 = out == W4_OUT_F32;
+    auto kernel = f32 ? rows_kernel<FMT, W4_OUT_F32, LOOKUP> : rows_kernel<FMT, W4_OUT_BF16, LOOKUP>;
+    return f4::launch_dependent(kernel, grid_for(T, K, f32 ? 128 : 256), kThreads, st, codes, scales,
+                                g, V, (int)K, ids, T, alpha, y, err);
 }
 
 }  // namespace
@@ -403,13 +402,10 @@ int f4_tensor_scale(const void* x, int in_dtype, int64_t R, int64_t K, float* g,
     if (ctas > cap) ctas = cap;
     if (ctas < 1) ctas = 1;  // no elements: g = 2^-100
     int* err = w4::device_error_word();
-    if (in_dtype == W4_IN_BF16)
-        tensor_scale_kernel<W4_IN_BF16><<<(int)ctas, kThreads, 0, st>>>(x, chunks, g, err);
-    else if (in_dtype == W4_IN_F32)
-        tensor_scale_kernel<W4_IN_F32><<<(int)ctas, kThreads, 0, st>>>(x, chunks, g, err);
-    else
-        tensor_scale_kernel<W4_IN_F16><<<(int)ctas, kThreads, 0, st>>>(x, chunks, g, err);
-    return w4::launch_status();
+    auto kernel = in_dtype == W4_IN_BF16  ? tensor_scale_kernel<W4_IN_BF16>
+                  : in_dtype == W4_IN_F32 ? tensor_scale_kernel<W4_IN_F32>
+                                          : tensor_scale_kernel<W4_IN_F16>;
+    return f4::launch_dependent(kernel, dim3((unsigned)ctas), kThreads, st, x, chunks, g, err);
 }
 
 int f4_quantize(const void* x, int in_dtype, int64_t R, int64_t K, int format, const float* g,
