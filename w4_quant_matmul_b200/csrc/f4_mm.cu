@@ -70,8 +70,9 @@ struct Cfg {
     static constexpr int sa_bytes = chunks * f4::kTileBytes;
     static constexpr int sb_bytes = chunks * f4::kTileBytes;
     static constexpr int stage_bytes = a_bytes + b_bytes + sa_bytes + sb_bytes;
-    // two CTAs run on an SM, so that one streams while the other starts or ends
-    static constexpr int stages = BN == 64 && FMT == W4_F4_NV ? 3 : 4;
+    // two CTAs run on an SM, so that one streams while the other starts or
+    // ends; each takes as many stages as its half holds
+    static constexpr int stages = (int)((kSmemTwo - 2048) / stage_bytes);
     static constexpr int acc_stages = 2;
     static constexpr int sf_cols = chunks * 4 * 2;  // TMEM columns per slot
     static constexpr int sf_slots = 2;
