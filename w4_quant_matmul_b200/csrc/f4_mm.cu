@@ -406,17 +406,16 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                     // K = 64 steps of this stage that hold elements
                     int steps = (p.K - ks * BK + kMmaK - 1) / kMmaK;
                     if (steps > BK / kMmaK) steps = BK / kMmaK;
-#pragma unroll
-                    for (int c = 0; c < C::chunks; ++c) {
-                        if (c * C::mma_per_chunk >= steps) break;
-                        copy_scales(sf + c * 4, scale_desc(sa + c * f4::kTileBytes));
-                        copy_scales(sfb + c * 4, scale_desc(sb + c * f4::kTileBytes));
-                    }
+                    // (a chunk's scales directly before its MMAs: see f4_pair.cu)
 #pragma unroll
                     for (int j = 0; j < BK / kMmaK; ++j) {
                         if (j >= steps) break;
                         const int c = j / C::mma_per_chunk;
                         const int id = j % C::mma_per_chunk * 2;
+                        if (id == 0) {
+                            copy_scales(sf + c * 4, scale_desc(sa + c * f4::kTileBytes));
+                            copy_scales(sfb + c * 4, scale_desc(sb + c * f4::kTileBytes));
+                        }
                         mma_f4<FMT>(d, operand_desc(a + j * (kMmaK / 2)),
                                     operand_desc(b + j * (kMmaK / 2)), instr_desc<FMT, BM, BN>(id),
                                     sf + c * 4, sfb + c * 4 + sb_col,

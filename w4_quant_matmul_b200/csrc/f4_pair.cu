@@ -10,9 +10,9 @@
 //              rows and their scale tiles (the weights' scales for all 192 rows:
 //              each CTA's TMEM needs them), all counted by the leader's barrier.
 //   warp 1     TMEM allocation; in the leader, scale copies and MMAs.
-//   warps 2-5  epilogue.  Tokens are TMEM lanes, so a thread holds consecutive
-//              columns of one row of y; a warp turns 32 rows x 128 bytes through
-//              shared memory and stores whole rows, 16 bytes a lane.
+//   warps 2-9  epilogue.  Tokens are TMEM lanes, so a thread holds consecutive
+//              columns of one row of y; a warp turns 32 rows x 32 columns through
+//              shared memory and stores them 16 bytes a lane, along the rows.
 // 192 columns is the widest tile whose accumulators fit TMEM twice beside the
 // scales (2 * 192 + 2 * 48 of 512 columns), so the epilogue of a tile runs under
 // the MMAs of the next.  192 rows of weights are one and a half scale tiles:
@@ -29,7 +29,9 @@ using namespace f4;
 constexpr int PM = 128;          // tokens of a CTA
 constexpr int PN = 192;          // weight rows of the pair
 constexpr int PH = PN / 2;       // staged by a CTA
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;     // two to a TMEM lane quarter
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kChunk = 32;       // columns that an epilogue warp stages at a time
 constexpr int kAccStages = 2;
 constexpr int kSfSlots = 2;
 
@@ -44,8 +46,8 @@ struct Cfg {
     static constexpr int stage_bytes = a_bytes + b_bytes + sa_bytes + sb_bytes;
     static constexpr int stages = FMT == W4_F4_MX ? 6 : 5;
     static constexpr int sf_cols = 3 * chunks * 4;  // 4 a chunk for tokens, 8 for weights
-    static constexpr int out = stages * stage_bytes;  // 4 KB a warp
-    static constexpr int bars = out + 4 * 4096;
+    static constexpr int out = stages * stage_bytes;  // 32 rows x kChunk columns a warp
+    static constexpr int bars = out + kEpiWarps * 32 * kChunk * 4;
     static constexpr int nbars = 2 * stages + 2 * kAccStages + 1;
     static constexpr int misc = bars + nbars * 8;
     static constexpr size_t total = (size_t)misc + 16 + 1024;
@@ -145,9 +147,13 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
         : "memory");
 }
 
-// 16-byte chunk j of row r of a warp's 32 x 128-byte staging tile: permuted so
-// that a column of chunks and a row of chunks both touch all banks.
-__device__ __forceinline__ uint32_t stage_at(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+// 16-byte piece j of row r of a warp's staging tile with `pieces` (4 or 8) to a
+// row, permuted so that a column of pieces and a row of them both spread over
+// all banks.
+template <int PIECES>
+__device__ __forceinline__ uint32_t stage_at(int r, int j) {
+    return r * (PIECES * 16) + ((j ^ ((PIECES == 8 ? r : r >> 1) & (PIECES - 1))) << 4);
+}
 
 template <int FMT, int OUT>
 __global__ void __launch_bounds__(kThreads)
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(kThreads)
         }
         for (int i = 0; i < kAccStages; ++i) {
             w4::mbar_init(&afull[i], 1);
-            w4::mbar_init(&aempty[i], 8);  // four epilogue warps of each CTA
+            w4::mbar_init(&aempty[i], 2 * kEpiWarps);
         }
         w4::mbar_init(drain, 1);
         *abort_flag = 0;
@@ -272,19 +278,21 @@ __global__ void __launch_bounds__(kThreads)
                     const uint32_t sfb = sf + C::chunks * 4;
                     int steps = (p.K - ks * BK + kMmaK - 1) / kMmaK;
                     if (steps > BK / kMmaK) steps = BK / kMmaK;
-#pragma unroll
-                    for (int c = 0; c < C::chunks; ++c) {
-                        if (c * C::mma_per_chunk >= steps) break;
-                        copy_scales_pair(sf + c * 4, scale_desc(sa + c * kTileBytes));
-                        copy_scales_pair(sfb + c * 8, scale_desc(sb + c * kTileBytes));
-                        copy_scales_pair(sfb + c * 8 + 4,
-                                         scale_desc(sb + C::sa_bytes + c * kTileBytes));
-                    }
+                    // a chunk's scales directly before its MMAs, where their copies
+                    // run beside the MMAs before (2048 x 19456 x 2560 of NV at
+                    // 1965 MHz: 46.5 us; all of a stage's copies first 49.8, each
+                    // chunk's one MMA earlier 50.8)
 #pragma unroll
                     for (int j = 0; j < BK / kMmaK; ++j) {
                         if (j >= steps) break;
                         const int c = j / C::mma_per_chunk;
                         const int id = j % C::mma_per_chunk * 2;
+                        if (id == 0) {
+                            copy_scales_pair(sf + c * 4, scale_desc(sa + c * kTileBytes));
+                            copy_scales_pair(sfb + c * 8, scale_desc(sb + c * kTileBytes));
+                            copy_scales_pair(sfb + c * 8 + 4,
+                                             scale_desc(sb + C::sa_bytes + c * kTileBytes));
+                        }
                         mma_pair<FMT>(d, operand_desc(a + j * (kMmaK / 2)),
                                       operand_desc(b + j * (kMmaK / 2)),
                                       instr_desc<FMT, 2 * PM, PN>(id), sf + c * 4,
@@ -304,10 +312,11 @@ __global__ void __launch_bounds__(kThreads)
         // ---------------- epilogue ----------------
         constexpr bool f32 = OUT == W4_OUT_F32;
         constexpr int esize = f32 ? 4 : 2;
-        constexpr int cols = 128 / esize;   // of a staged chunk
-        constexpr int vec = 16 / esize;     // of a 16-byte store
-        const int quarter = warp & 3;
-        uint8_t* st = smem + C::out + quarter * 4096;
+        constexpr int vec = 16 / esize;             // columns of a 16-byte piece
+        constexpr int pieces = kChunk / vec;        // 16-byte pieces of a staged row
+        constexpr int rows_step = 32 / pieces;      // rows that a warp stores at once
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t* st = smem + C::out + (warp - 2) * 32 * kChunk * 4;
         pdl_wait();
         const float alpha = FMT == W4_F4_NV ? __fmul_rn(__ldg(p.gw), __ldg(p.ga)) : 1.0f;
         const bool aligned = p.N % vec == 0;  // rows of y start on 16 bytes
@@ -319,68 +328,62 @@ __global__ void __launch_bounds__(kThreads)
             if (!w4::mbar_wait(&afull[as], (uint32_t)(ti / kAccStages) & 1u, abort_flag, p.err)) break;
             tc_fence_after();
             const uint32_t acc = tmem + as * PN + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-            for (int c0 = 0; c0 < PN; c0 += cols) {
+            // chunks half, half + 2, half + 4; each is on its way from TMEM while
+            // the one before it is stored
+            uint32_t r[32];
+            tmem_ld32(acc + half * kChunk, r);
+#pragma unroll
+            for (int i3 = 0; i3 < PN / kChunk / 2; ++i3) {
+                const int c0 = (2 * i3 + half) * kChunk;
                 const int n0 = tn * PN + c0;
-                uint32_t w[32];  // 128 bytes of this lane's row
-                if constexpr (f32) {
-                    tmem_ld32(acc + c0, w);
-                    tmem_wait32(w);
+                tmem_wait32(r);
+                __syncwarp();  // the previous chunk has been read
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-                } else {
-                    uint32_t r0[32], r1[32];
-                    tmem_ld32(acc + c0, r0);
-                    tmem_ld32(acc + c0 + 32, r1);
-                    tmem_wait32(r0);
-                    tmem_wait32(r1);
+                for (int j = 0; j < pieces; ++j) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r0[2 * i]) * alpha,
-                                                                 __uint_as_float(r0[2 * i + 1]) * alpha);
-                        w[i] = *reinterpret_cast<uint32_t*>(&h);
-                        h = __floats2bfloat162_rn(__uint_as_float(r1[2 * i]) * alpha,
-                                                  __uint_as_float(r1[2 * i + 1]) * alpha);
-                        w[16 + i] = *reinterpret_cast<uint32_t*>(&h);
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (f32) {
+                            w[i] = __float_as_uint(__uint_as_float(r[4 * j + i]) * alpha);
+                        } else {
+                            const __nv_bfloat162 h =
+                                __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * i]) * alpha,
+                                                      __uint_as_float(r[8 * j + 2 * i + 1]) * alpha);
+                            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
                     }
+                    *reinterpret_cast<uint4*>(st + stage_at<pieces>(lane, j)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (c0 + cols >= PN) {  // the accumulators are in registers
+                __syncwarp();
+                if (i3 + 1 < PN / kChunk / 2) {
+                    tmem_ld32(acc + c0 + 2 * kChunk, r);
+                } else {  // the accumulators have been read
                     tc_fence_before();
-                    __syncwarp();
                     if (lane == 0) arrive_at(in_cta(&aempty[as], 0));
                 }
                 if (t0 >= p.M || n0 >= p.N) continue;
-                __syncwarp();  // the previous chunk has been read
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(st + stage_at(lane, j)) =
-                        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                __syncwarp();
                 if (aligned) {
-                    // four rows a step, eight lanes of 16 bytes each
-                    const int j = lane & 7;
+                    const int j = lane % pieces;
                     const bool in = n0 + (j + 1) * vec <= p.N;
+                    uint8_t* y = static_cast<uint8_t*>(p.y) +
+                                 ((int64_t)(t0 + lane / pieces) * p.N + n0 + j * vec) * esize;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const uint4 v = *reinterpret_cast<const uint4*>(st + stage_at(r, j));
-                        if (in && t0 + r < p.M)
-                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) +
-                                                      ((int64_t)(t0 + r) * p.N + n0 + j * vec) * esize) = v;
+                    for (int i = 0; i < pieces; ++i) {
+                        const int row = i * rows_step + lane / pieces;
+                        const uint4 v = *reinterpret_cast<const uint4*>(st + stage_at<pieces>(row, j));
+                        if (in && t0 + row < p.M)
+                            *reinterpret_cast<uint4*>(y + (int64_t)i * rows_step * p.N * esize) = v;
                     }
-                } else {
-                    for (int r = 0; r < 32 && t0 + r < p.M; ++r) {
-#pragma unroll
-                        for (int c = lane; c < cols; c += 32) {
-                            if (n0 + c >= p.N) continue;
-                            const uint32_t at = stage_at(r, c / vec) + c % vec * esize;
-                            const int64_t o = (int64_t)(t0 + r) * p.N + n0 + c;
-                            if constexpr (f32)
-                                static_cast<uint32_t*>(p.y)[o] = *reinterpret_cast<uint32_t*>(st + at);
-                            else
-                                static_cast<uint16_t*>(p.y)[o] = *reinterpret_cast<uint16_t*>(st + at);
-                        }
+                } else if (n0 + lane < p.N) {  // one column a lane
+                    const uint32_t in_piece = lane % vec * esize;
+                    for (int row = 0; row < 32 && t0 + row < p.M; ++row) {
+                        const uint8_t* v = st + stage_at<pieces>(row, lane / vec) + in_piece;
+                        const int64_t o = (int64_t)(t0 + row) * p.N + n0 + lane;
+                        if constexpr (f32)
+                            static_cast<uint32_t*>(p.y)[o] = *reinterpret_cast<const uint32_t*>(v);
+                        else
+                            static_cast<uint16_t*>(p.y)[o] = *reinterpret_cast<const uint16_t*>(v);
                     }
                 }
             }
