@@ -770,6 +770,7 @@ int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStre
     // tile starts on one
     if (p.M <= 16) return launch_tiles<FMT, 16, kMm>(codes, qa, p, st);
     if (p.M <= 32) return launch_tiles<FMT, 32, kMm>(codes, qa, p, st);
+    if (p.M <= 48) return launch_tiles<FMT, 48, kMm>(codes, qa, p, st);
     return launch_tiles<FMT, 64, kMm>(codes, qa, p, st);
 }
 
@@ -783,6 +784,7 @@ int launch_fused(const uint8_t* codes, const Params& p, cudaStream_t st) {
 template <int FMT>
 int launch_planes(const uint8_t* codes, const uint8_t* digits, const Params& p, cudaStream_t st) {
     if (p.M <= 4) return launch_tiles<FMT, 32, kGemvPlanes>(codes, digits, p, st);
+    if (p.M <= 6) return launch_tiles<FMT, 48, kGemvPlanes>(codes, digits, p, st);
     return launch_tiles<FMT, 64, kGemvPlanes>(codes, digits, p, st);
 }
 
