@@ -48,7 +48,7 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 
 // Programmatic dependent launch.  Every f4 kernel waits for the kernel before it
 // ahead of its first access to global memory (f4_gemv's product: to anything but
-// weights) and only then lets the kernel after it start, so that a kernel that
+// weights; the tensor scale: to anything but x) and only then lets the kernel after it start, so that a kernel that
 // starts early is one ahead of what has completed, never two.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
