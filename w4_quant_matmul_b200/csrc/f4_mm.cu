@@ -284,7 +284,41 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     const int kb = (int)((int64_t)p.stages_k * split / p.splits);
     const int ke = (int)((int64_t)p.stages_k * (split + 1) / p.splits);
 
+    const int chunks_last = p.tiles_k - (p.stages_k - 1) * C::chunks;
+    auto chunks_of = [&](int ks) { return ks + 1 < p.stages_k ? C::chunks : chunks_last; };
+    auto load_a = [&](int s, int ks, int tn) {
+        const int ch = chunks_of(ks);
+        w4::mbar_arrive_expect_tx(&full[s], C::a_bytes + ch * f4::kTileBytes +
+                                                (FUSED ? 0 : C::b_bytes + ch * f4::kTileBytes));
+        uint8_t* st = smem + s * C::stage_bytes;
+        w4::tma_load_2d(st, &tm_a, &full[s], ks * kRowBytes, tn * BM);
+        w4::bulk_load_1d(st + C::a_bytes + C::b_bytes,
+                         p.sa + ((int64_t)tn * p.tiles_k + (int64_t)ks * C::chunks) *
+                                    f4::kTileBytes,
+                         (uint32_t)(ch * f4::kTileBytes), &full[s]);
+    };
+    auto load_b = [&](int s, int ks, int tm) {
+        const int ch = chunks_of(ks);
+        uint8_t* st = smem + s * C::stage_bytes;
+        w4::tma_load_2d(st + C::a_bytes, &tm_b, &full[s], ks * kRowBytes, tm * BN);
+        w4::bulk_load_1d(st + C::a_bytes + C::b_bytes + C::sa_bytes,
+                         p.sb + ((int64_t)(tm * BN / f4::kRowTile) * p.tiles_k +
+                                 (int64_t)ks * C::chunks) *
+                                    f4::kTileBytes,
+                         (uint32_t)(ch * f4::kTileBytes), &full[s]);
+    };
+
+    // f4_gemv with digit planes: the first tile's first weights are requested
+    // ahead of the set-up that all warps share, and of the wait for the digit
+    // kernel (which started this one when everything before it was complete).
+    // The other modes have to wait first, and set up meanwhile.
+    int pre = 0;
+    if constexpr (MODE == kGemvPlanes)
+        if (first < tiles) pre = ke - kb < C::stages ? ke - kb : C::stages;
+
     if (threadIdx.x == 0) {
+        w4::prefetch_tmap(&tm_a);
+        if constexpr (!FUSED) w4::prefetch_tmap(&tm_b);
         for (int i = 0; i < C::stages; ++i) {
             // the producer, and a digit warp for each token
             w4::mbar_init(&full[i], FUSED ? 1 + p.M : 1);
@@ -297,6 +331,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         w4::mbar_init(drain, 1);
         *abort_flag = 0;
         w4::fence_mbar_init();
+        for (int i = 0; i < pre; ++i) load_a(i, kb + i, first);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -313,42 +348,8 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (w4::elect_one()) {
-            w4::prefetch_tmap(&tm_a);
-            if constexpr (!FUSED) w4::prefetch_tmap(&tm_b);
-            const int chunks_last = p.tiles_k - (p.stages_k - 1) * C::chunks;
-            auto chunks_of = [&](int ks) { return ks + 1 < p.stages_k ? C::chunks : chunks_last; };
-            auto load_a = [&](int s, int ks, int tn) {
-                const int ch = chunks_of(ks);
-                w4::mbar_arrive_expect_tx(&full[s], C::a_bytes + ch * f4::kTileBytes +
-                                                        (FUSED ? 0 : C::b_bytes + ch * f4::kTileBytes));
-                uint8_t* st = smem + s * C::stage_bytes;
-                w4::tma_load_2d(st, &tm_a, &full[s], ks * kRowBytes, tn * BM);
-                w4::bulk_load_1d(st + C::a_bytes + C::b_bytes,
-                                 p.sa + ((int64_t)tn * p.tiles_k + (int64_t)ks * C::chunks) *
-                                            f4::kTileBytes,
-                                 (uint32_t)(ch * f4::kTileBytes), &full[s]);
-            };
-            auto load_b = [&](int s, int ks, int tm) {
-                const int ch = chunks_of(ks);
-                uint8_t* st = smem + s * C::stage_bytes;
-                w4::tma_load_2d(st + C::a_bytes, &tm_b, &full[s], ks * kRowBytes, tm * BN);
-                w4::bulk_load_1d(st + C::a_bytes + C::b_bytes + C::sa_bytes,
-                                 p.sb + ((int64_t)(tm * BN / f4::kRowTile) * p.tiles_k +
-                                         (int64_t)ks * C::chunks) *
-                                            f4::kTileBytes,
-                                 (uint32_t)(ch * f4::kTileBytes), &full[s]);
-            };
             int it = 0;  // stages issued
             bool ok = true;
-            // the weights do not depend on the digit kernel that precedes this
-            // one, so the first stages' are requested before the wait for it
-            // (that kernel starts this one only after everything before it has
-            // completed)
-            int pre = 0;
-            if constexpr (MODE == kGemvPlanes) {
-                if (first < tiles) pre = ke - kb < C::stages ? ke - kb : C::stages;
-                for (int i = 0; i < pre; ++i) load_a(i, kb + i, first % p.tiles_n);
-            }
             pdl_wait();
             pdl_trigger();
             for (int tile = first; tile < tiles && ok; tile += step) {
