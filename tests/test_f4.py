@@ -304,6 +304,22 @@ def test_gemv_activation_range(torch, w4, fmt):
     assert (y[2] == 0).all()
 
 
+def test_gemv_small_scales(torch, w4):
+    # a tensor scale and activations whose product leaves the range of fp32,
+    # with weights that bring the sums back into it
+    N, K = 130, 64
+    codes = np.full((N, K), 7, np.uint8)                          # 6
+    scales = np.full((N, K // 16), 126, np.uint8)                 # 448
+    g = 2.0 ** -100
+    w = Matrix(torch, codes, scales, "nv", g)
+    for M in (1, 5):
+        x = np.full((M, K), 2.0 ** -28)
+        y = host(w4.f4_gemv(*w.planes, dev(torch, x).bfloat16(), out_dtype=torch.float32))
+        # every digit, weight and partial sum is a small integer times a power
+        # of two: exact
+        assert np.array_equal(y.astype(np.float64), x @ w.scaled.T)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_nan_stays_in_its_row(torch, w4, fmt):
     N, K, M = 140, 160, 6
@@ -525,6 +541,147 @@ def test_workspace_too_small_is_refused(torch, w4):
                    workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert (y == 9).all()
+
+
+CAPTURE_FIRST = """
+import torch, w4_quant_matmul_b200 as w4
+x = torch.randn(40, 288, device="cuda").bfloat16()
+w = torch.randn(300, 288, device="cuda")
+ids = torch.tensor([3, -1, 299], device="cuda")
+out = {}
+def step():
+    for fmt in ("mx", "nv"):
+        p, a = w4.f4_quantize(w, fmt), w4.f4_quantize(x, fmt)
+        out[fmt] = [w4.f4_mm(*p, *a), w4.f4_gemv(*p, x[:1]), w4.f4_gemv(*p, x[:8]),
+                    w4.f4_embed(*p, ids), w4.f4_dequantize(*p)]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):       # the first calls of the process
+    step()
+graphed = {k: list(v) for k, v in out.items()}
+for r in range(2):
+    g.replay()
+torch.cuda.synchronize()
+step()
+torch.cuda.synchronize()
+for fmt in out:
+    for a, b in zip(graphed[fmt], out[fmt]):
+        assert torch.equal(a, b)
+w4.w4_check_device_error()
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture(torch):
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], cwd=ROOT, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, (r.stdout, r.stderr[-3000:])
+
+
+def test_two_host_threads(torch, w4):
+    """Two threads, each with its own stream and tensors, calling at once."""
+    import threading
+    bad = []
+
+    def work(seed, fmt):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            w = random_matrix(torch, 1500, 544, fmt, seed)
+            x = dev(torch, activations(6, 544, seed + 1)).bfloat16()
+            src = dev(torch, activations(150, 544, seed + 2)).bfloat16()
+            want = None
+            for i in range(40):
+                q = w4.f4_quantize(src, fmt)
+                got = [w4.f4_gemv(*w.planes, x), w4.f4_gemv(*w.planes, x[:1]),
+                       w4.f4_mm(*w.planes, *q), q[0]]
+                s.synchronize()
+                if want is None:
+                    want = got
+                elif not all(torch.equal(a, b) for a, b in zip(want, got)):
+                    bad.append((seed, i))
+
+    threads = [threading.Thread(target=work, args=(100 * i, FORMATS[i % 2])) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    w4.w4_check_device_error()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_chain_of_dependent_products(torch, w4, fmt):
+    """Products fed each other's outputs back to back, every buffer poisoned
+    before: each kernel starts while the one before it still runs and has to
+    wait for its results."""
+    D = 512
+    ws = [w4.f4_quantize(dev(torch, np.random.default_rng(i).standard_normal((D, D)) / 20)
+                         .float(), fmt) for i in range(6)]
+    for M in (1, 4, 7):
+        x0 = dev(torch, activations(M, D, 7)).bfloat16()
+        want, x = [], x0
+        for p in ws:
+            x = w4.f4_gemv(*p, x)
+            torch.cuda.synchronize()
+            want.append(x.clone())
+        ys = [torch.empty((M, D), dtype=torch.bfloat16, device="cuda") for _ in ws]
+        for _ in range(5):
+            for y in ys:
+                y.fill_(float("nan"))
+            x = x0
+            for p, y in zip(ws, ys):
+                x = w4.f4_gemv(*p, x, y=y)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(ys, want))
+    for M in (40, 300):
+        x0 = dev(torch, activations(M, D, 8)).bfloat16()
+        want, x = [], x0
+        for p in ws:
+            q = w4.f4_quantize(x, fmt)
+            torch.cuda.synchronize()
+            x = w4.f4_mm(*p, *q)
+            torch.cuda.synchronize()
+            want.append(x.clone())
+        for _ in range(5):
+            got, x = [], x0
+            for p in ws:
+                x = w4.f4_mm(*p, *w4.f4_quantize(x, fmt))
+                got.append(x)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_beside_the_integer_format(torch, w4):
+    """f4 kernels between the library's other kernels, which start early too:
+    every result as when each kernel runs alone."""
+    N, K = 512, 512
+    src = dev(torch, np.random.default_rng(3).standard_normal((N, K))).float()
+    x = dev(torch, activations(4, K, 4)).bfloat16()
+
+    def step(sync):
+        def done(*t):
+            if sync:
+                torch.cuda.synchronize()
+            return t
+        codes, d, m = done(*w4.w4_pack(src))
+        f = w4.f4_quantize(src, "nv")
+        done()
+        y = w4.w4_gemv(codes, d, m, x)
+        done()
+        z = w4.f4_gemv(*f, y)
+        done()
+        q = w4.q8_quantize_act(z)
+        done()
+        u = w4.w4a8_mmq(codes, d, m, *q)
+        done()
+        v = w4.f4_mm(*f, *w4.f4_quantize(u, "nv"))
+        done()
+        t = w4.w4a8_gemv_bf16(codes, d, m, v)
+        torch.cuda.synchronize()
+        return [y, z, *q, u, v, t]
+
+    want = step(True)
+    for _ in range(8):
+        assert all(torch.equal(a, b) for a, b in zip(step(False), want))
 
 
 @pytest.mark.skipif(os.environ.get("W4_LIBRARY") == "debug", reason="runs this file's cases itself")

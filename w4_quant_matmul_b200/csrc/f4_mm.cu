@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                         for (int j = 6; j >= 0; --j)
                             v = fmaf(v, 0.125f, __uint_as_float(r[8 * h + j]));
                         if (t < p.M) {
-                            if constexpr (FMT == W4_F4_NV) v *= factor(t) * alpha;
+                            // (one at a time: their product could leave the range of fp32)
+                            if constexpr (FMT == W4_F4_NV) v = v * factor(t) * alpha;
                             if (p.splits > 1)
                                 part[t * BM + row] = v;
                             else if (n < p.N)
