@@ -19,7 +19,7 @@ per-token chain (36 layers x 4 shapes + lm_head, tok/s-equivalent).
 
 One JSON line is printed by rank 0.  `--impl reference` times the CPU oracle
 on a bounded sample of the same workload instead.  `--case gemv|gemv_g32|mmq|
-quant` launches one kernel configuration `--reps` times (the commands the
+quant|f4_mm|...` launches one kernel configuration `--reps` times (the commands the
 committed ncu summaries capture); with `--time` each launch is timed alone.
 """
 from __future__ import annotations
@@ -881,6 +881,35 @@ def run_reference(args):
     print(json.dumps(line), flush=True)
 
 
+def f4_case(args, w4, torch, dev, g):
+    """A launch of one f4_* operator on caller-owned outputs, and its algorithmic
+    bytes: f4_quant reads bf16 x [M][K], f4_dequant writes bf16 [M][K], f4_embed
+    looks M rows up in a table [N][K], f4_gemv and f4_mm multiply by [N][K]."""
+    N, K, M, fmt = args.N, args.K, args.M, args.format
+    size = lambda *ts: sum(t.numel() * t.element_size() for t in ts if t is not None)
+    x = torch.randn((M, K), generator=g, device=dev).to(torch.bfloat16)
+    if args.case in ("f4_quant", "f4_dequant"):
+        codes, scales, ts = w4.f4_quantize(x, fmt)
+        if args.case == "f4_quant":
+            return (lambda: w4.f4_quantize(x, fmt, ts, codes, scales)), size(x, codes, scales)
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        return (lambda: w4.f4_dequantize(codes, scales, ts, y=y)), size(y, codes, scales)
+    w = torch.randn((N, K), generator=g, device=dev, dtype=torch.float32).mul_(0.02)
+    planes = w4.f4_quantize(w, fmt)
+    del w
+    if args.case == "f4_embed":
+        ids = torch.randint(0, N, (M,), generator=g, device=dev)
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        row = size(planes[0]) // N + K // (32 if fmt == "mx" else 16)
+        return (lambda: w4.f4_embed(*planes, ids, y=y)), M * row + size(ids, y)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    if args.case == "f4_gemv":
+        ws = torch.empty(w4.f4_gemv_workspace_size(M, N, K, fmt), dtype=torch.uint8, device=dev)
+        return (lambda: w4.f4_gemv(*planes, x, y=y, workspace=ws)), size(*planes, x, y)
+    acts = w4.f4_quantize(x, fmt)
+    return (lambda: w4.f4_mm(*planes, *acts, y=y)), size(*planes, *acts, y)
+
+
 def run_case(args):
     """One kernel configuration launched `--reps` times on device-resident
     synthetic inputs (the command the committed ncu summaries capture).  With
@@ -895,51 +924,56 @@ def run_case(args):
     g = torch.Generator(device=dev)
     g.manual_seed(17)
     N, K, M = args.N, args.K, args.M
-    w = torch.randn((N, K), generator=g, device=dev, dtype=torch.float32).mul_(0.02)
-    codes, d, m = (w4.w4_pack_g32 if args.case == "gemv_g32" else w4.w4_pack)(w)
-    del w
-    torch.cuda.synchronize()
-    x = torch.randn((M, K), generator=g, device=dev).to(torch.bfloat16)
-    nbytes = None
-    if args.case in ("gemv", "gemv_g32"):
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        gemv = w4.w4_gemv_g32 if args.case == "gemv_g32" else w4.w4_gemv
-        nbytes = sum(t.numel() * t.element_size() for t in (codes, d, m, x, y))
-
-        def launch():
-            gemv(codes, d, m, x, out_dtype=torch.bfloat16, y=y)
-    elif args.case == "quant":
-        qa, dx, S = w4.q8_quantize_act(x)
-        nbytes = quant_bytes(M, K)
-
-        def launch():
-            w4.q8_quantize_act(x, qa, dx, S)
-    elif args.case in ("w4a8_gemv", "w4a8_gemv_bf16"):
-        qa, dx, S = w4.q8_quantize_act(x)
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        if args.case == "w4a8_gemv":
-            nbytes = w4a8_gemv_bytes(N, K, M)
-
-            def launch():
-                w4.w4a8_gemv(codes, d, m, qa, dx, S, out_dtype=torch.bfloat16, y=y)
-        else:
-            nbytes = gemv_bytes(N, K, M)
-
-            def launch():
-                w4.w4a8_gemv_bf16(codes, d, m, x, out_dtype=torch.bfloat16, y=y)
-    elif args.case == "pack":
-        w = torch.randn((N, K), generator=g, device=dev, dtype=torch.float32).mul_(0.02)
-        nbytes = N * K * 4 + N * K // 2 + N * (K // GROUP) * 4
-
-        def launch():
-            w4.w4_pack(w, codes, d, m)
+    if args.case.startswith("f4_"):
+        launch, nbytes = f4_case(args, w4, torch, dev, g)
     else:
-        qa, dx, S = w4.q8_quantize_act(x)
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        w = torch.randn((N, K), generator=g, device=dev, dtype=torch.float32).mul_(0.02)
+        codes, d, m = (w4.w4_pack_g32 if args.case == "gemv_g32" else w4.w4_pack)(w)
+        del w
+        torch.cuda.synchronize()
+        x = torch.randn((M, K), generator=g, device=dev).to(torch.bfloat16)
+        nbytes = None
+        if args.case in ("gemv", "gemv_g32"):
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+            gemv = w4.w4_gemv_g32 if args.case == "gemv_g32" else w4.w4_gemv
+            nbytes = sum(t.numel() * t.element_size() for t in (codes, d, m, x, y))
 
-        def launch():
-            w4.w4a8_mmq(codes, d, m, qa, dx, S, out_dtype=torch.bfloat16, y=y)
+            def launch():
+                gemv(codes, d, m, x, out_dtype=torch.bfloat16, y=y)
+        elif args.case == "quant":
+            qa, dx, S = w4.q8_quantize_act(x)
+            nbytes = quant_bytes(M, K)
+
+            def launch():
+                w4.q8_quantize_act(x, qa, dx, S)
+        elif args.case in ("w4a8_gemv", "w4a8_gemv_bf16"):
+            qa, dx, S = w4.q8_quantize_act(x)
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+            if args.case == "w4a8_gemv":
+                nbytes = w4a8_gemv_bytes(N, K, M)
+
+                def launch():
+                    w4.w4a8_gemv(codes, d, m, qa, dx, S, out_dtype=torch.bfloat16, y=y)
+            else:
+                nbytes = gemv_bytes(N, K, M)
+
+                def launch():
+                    w4.w4a8_gemv_bf16(codes, d, m, x, out_dtype=torch.bfloat16, y=y)
+        elif args.case == "pack":
+            w = torch.randn((N, K), generator=g, device=dev, dtype=torch.float32).mul_(0.02)
+            nbytes = N * K * 4 + N * K // 2 + N * (K // GROUP) * 4
+
+            def launch():
+                w4.w4_pack(w, codes, d, m)
+        else:
+            qa, dx, S = w4.q8_quantize_act(x)
+            y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+
+            def launch():
+                w4.w4a8_mmq(codes, d, m, qa, dx, S, out_dtype=torch.bfloat16, y=y)
     out = {"case": args.case, "N": N, "K": K, "M": M, "reps": args.reps}
+    if args.case.startswith("f4_"):
+        out["format"] = args.format
     if args.time:
         # the launch is captured once in a CUDA graph and replayed between the
         # events, so that host-side call overhead never idles the GPU inside
@@ -966,7 +1000,7 @@ def run_case(args):
         if nbytes is not None:
             out["bytes"] = nbytes
             out["GBps"] = round(nbytes / (us * 1e-6) / 1e9, 1)
-        if args.case == "mmq":
+        if args.case in ("mmq", "f4_mm"):
             out["TOPS"] = round(mmq_ops(M, N, K) / (us * 1e-6) / 1e12, 1)
     else:
         for _ in range(args.reps):
@@ -1011,8 +1045,11 @@ def main(argv=None):
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-seconds", type=float, default=15.0)
     ap.add_argument("--case", choices=["gemv", "gemv_g32", "mmq", "quant", "w4a8_gemv",
-                                       "w4a8_gemv_bf16", "pack", "chain", "sweep"],
+                                       "w4a8_gemv_bf16", "pack", "chain", "sweep", "f4_quant",
+                                       "f4_dequant", "f4_embed", "f4_gemv", "f4_mm"],
                     help="launch one kernel configuration --reps times (profiling)")
+    ap.add_argument("--format", choices=["mx", "nv"], default="mx",
+                    help="with --case f4_*: the 4-bit floating-point format")
     ap.add_argument("--time", action="store_true",
                     help="with --case: time each launch alone after an L2 flush")
     ap.add_argument("--N", type=int, default=151936)

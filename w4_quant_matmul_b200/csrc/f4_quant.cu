@@ -110,15 +110,19 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     return r;
 }
 
-// Two e2m1 codes (low 8 bits) -> fp32.  An e2m1 number has the layout of fp16's
-// top bits, sign, exponent, one mantissa bit, with the exponent 14 lower
-// (subnormals included): the bits moved there are the number times 2^-14.
-__device__ __forceinline__ void from_e2m1x2(uint32_t c, float* v) {
-    const uint32_t w = (c & 0xFu) | ((c & 0xF0u) << 12);
-    const uint32_t h = ((w & 0x00080008u) << 12) | ((w & 0x00070007u) << 9);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[0] = f.x * 16384.0f;
-    v[1] = f.y * 16384.0f;
+// Four e2m1 codes (low 16 bits) -> fp32.  As fp16 their low bytes are zero; the
+// high bytes come from two byte permutations that use the codes as selectors,
+// one for the magnitudes and one for the signs.
+__device__ __forceinline__ void from_e2m1x4(uint32_t c, float* v) {
+    const uint32_t mag = __byte_perm(0x3E3C3800u, 0x46444240u, c & 0x7777u);
+    const uint32_t top = mag | __byte_perm(0x00008000u, 0u, (c >> 3) & 0x1111u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t h = __byte_perm(top, 0u, i ? 0x3424 : 0x1404);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -351,11 +355,14 @@ __global__ void __launch_bounds__(kThreads)
         if (k >= K) break;
         float v[kElems];
 #pragma unroll
-        for (int i = 0; i < kElems; i += 2) from_e2m1x2(q[u] >> (4 * i), v + i);
+        for (int i = 0; i < kElems; i += 4) from_e2m1x4(q[u] >> (4 * i), v + i);
         const float s = f4::scale_value<FMT>(sb[u]);
 #pragma unroll
-        for (int i = 0; i < kElems; ++i)
-            v[i] = live ? __fmul_rn(__fmul_rn(v[i], s), c) : 0.0f;
+        for (int i = 0; i < kElems; ++i) {
+            v[i] = __fmul_rn(v[i], s);  // exact
+            if constexpr (LOOKUP || FMT == W4_F4_NV) v[i] = __fmul_rn(v[i], c);
+            if constexpr (LOOKUP) v[i] = live ? v[i] : 0.0f;
+        }
         if constexpr (OUT == W4_OUT_F32) {
             *reinterpret_cast<float4*>(static_cast<float*>(y) + t * K + k) =
                 make_float4(v[0], v[1], v[2], v[3]);
