@@ -41,15 +41,16 @@
  *     the access (a stand-in for a memory checker; for tests on small shapes).
  *   - Results are bitwise deterministic run to run (fixed reduction orders, no
  *     floating-point atomics).
- *   - The decode GEMVs (w4_gemv, w4a8_gemv, w4a8_gemv_bf16) and the W4A8
- *     product (w4a8_mmq and its variants, when it needs no workspace) are
+ *   - The decode GEMVs (w4_gemv, w4a8_gemv, w4a8_gemv_bf16, f4_gemv) and the
+ *     W4A8 product (w4a8_mmq and its variants, when it needs no workspace) are
  *     launched with programmatic dependent launch and read their weight
- *     planes (codes, d, m) without waiting for the kernel launched
+ *     planes (codes, d, m; codes, scales) without waiting for the kernel launched
  *     immediately before them on the same stream (their activations are read
  *     only after that kernel has completed).  The weight planes must
  *     therefore not be written by that immediately preceding kernel: pack
  *     weights in an earlier launch, or put an event, a synchronisation or any
- *     other launch in between.
+ *     other launch in between.  (f4_quantize may directly precede f4_gemv: it
+ *     does not let the next kernel start before it has completed.)
  */
 #ifndef W4_H
 #define W4_H

@@ -47,9 +47,11 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 }
 
 // Programmatic dependent launch.  Every f4 kernel waits for the kernel before it
-// ahead of its first access to global memory (f4_gemv's product: to anything but
-// weights; the tensor scale: to anything but x) and only then lets the kernel after it start, so that a kernel that
-// starts early is one ahead of what has completed, never two.
+// ahead of its first access to global memory -- f4_gemv's product: to anything but
+// weights; the tensor scale: to anything but x, which the kernel before it never
+// writes -- and lets the kernel after it start once it has waited (the digit
+// kernel of f4_gemv at once).  The quantiser, which writes what f4_gemv reads
+// early, does not let the next kernel start early at all.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

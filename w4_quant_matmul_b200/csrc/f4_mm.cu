@@ -247,6 +247,9 @@ __device__ __forceinline__ void digits8(const uint4& raw, bool live, int emax, i
 // stage, which one SM's share of HBM delivers every 850.
 constexpr int digit_warps(int bn) { return bn / kDigits * 2; }
 
+// Whether CTAs of a grid without K slices work on several tiles each.
+__host__ __device__ constexpr bool many_tiles(int64_t tiles, int64_t ctas) { return tiles > ctas; }
+
 constexpr int threads_of(int bn, Mode mode) {
     return 32 * (kDigitWarp0 + (mode == kGemvFused ? digit_warps(bn) : 0));
 }
@@ -308,13 +311,16 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                          (uint32_t)(ch * f4::kTileBytes), &full[s]);
     };
 
-    // f4_gemv with digit planes: the first tile's first weights are requested
-    // ahead of the set-up that all warps share, and of the wait for the digit
-    // kernel (which started this one when everything before it was complete).
-    // The other modes have to wait first, and set up meanwhile.
+    // f4_gemv: the first tile's first weights are requested ahead of the set-up
+    // that all warps share and of the wait for the kernel before (w4.h says which
+    // kernels may not be it).  With the digits made here only where a CTA has
+    // several tiles to stream: lm_head 33.0 -> 31.5 us in a row of them, but
+    // 19456 x 2560 6.6 -> 7.8, where the requests delay what the kernel before
+    // still has to load.
     int pre = 0;
-    if constexpr (MODE == kGemvPlanes)
-        if (first < tiles) pre = ke - kb < C::stages ? ke - kb : C::stages;
+    if constexpr (GEMV)
+        if (first < tiles && (!FUSED || many_tiles(tiles, gridDim.x)))
+            pre = ke - kb < C::stages ? ke - kb : C::stages;
 
     if (threadIdx.x == 0) {
         w4::prefetch_tmap(&tm_a);
@@ -641,11 +647,14 @@ constexpr int kDigitElems = kDigitThreads * 8;  // k of one block of threads
 template <int FMT>
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const uint16_t* __restrict__ x, int K, uint8_t* __restrict__ codes,
-                  uint8_t* __restrict__ scales, float* __restrict__ row_factor, int* err) {
-    // after the wait all that came before is complete: the product may start,
-    // and read the weights before it waits for this kernel
+                  uint8_t* __restrict__ scales, float* __restrict__ row_factor, bool early,
+                  int* err) {
+    // the product may start and read its weights; it waits for this kernel, and
+    // so for all before it, ahead of anything else.  Where it streams several
+    // tiles a CTA it starts before this kernel's own wait.
+    if (early) pdl_trigger();
     pdl_wait();
-    pdl_trigger();
+    if (!early) pdl_trigger();
     constexpr int kWordLanes = block_of(FMT) / 2;
     const int t = blockIdx.y;
     const int lane = threadIdx.x & 31;
@@ -901,7 +910,8 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     const int kpad = p.tiles_k * 4 * f4::block_of(format);
     const dim3 grid((unsigned)((kpad + kDigitElems - 1) / kDigitElems), (unsigned)M);
     rc = launch_dependent(nv ? digits_kernel<W4_F4_NV> : digits_kernel<W4_F4_MX>, grid, kDigitThreads,
-                          st, x_bf16, (int)K, base, base + ws.scales, factors, p.err);
+                          st, x_bf16, (int)K, base, base + ws.scales, factors,
+                          many_tiles(row_tiles(N), (int64_t)w4::sm_count() * 2), p.err);
     if (rc != W4_OK) return rc;
     return nv ? launch_planes<W4_F4_NV>(codes, base, p, st)
               : launch_planes<W4_F4_MX>(codes, base, p, st);

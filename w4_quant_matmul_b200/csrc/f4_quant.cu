@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
                                                             uint8_t* __restrict__ scales,
                                                             int* err) {
     f4::pdl_wait();
-    f4::pdl_trigger();
+    // no early start for the kernel after this one: it may be f4_gemv, which reads
+    // the planes written here before it waits
     constexpr int kElems = quant_elems(FMT), kOct = kElems / 8;
     constexpr int kU = kSegs / kOct;
     constexpr int kSpan = 32 * kElems;
