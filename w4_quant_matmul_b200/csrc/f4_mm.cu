@@ -72,7 +72,7 @@ struct Cfg {
     static constexpr int stage_bytes = a_bytes + b_bytes + sa_bytes + sb_bytes;
     // two CTAs run on an SM, so that one streams while the other starts or
     // ends; each takes as many stages as its half holds
-    static constexpr int stages = (int)((kSmemTwo - 2048) / stage_bytes);
+    static constexpr int stages = (int)((kSmemTwo - 512) / stage_bytes);
     static constexpr int acc_stages = 2;
     static constexpr int sf_cols = chunks * 4 * 2;  // TMEM columns per slot
     static constexpr int sf_slots = 2;
@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int bars = stages * stage_bytes;
     static constexpr int misc = bars + nbars * 8;      // TMEM base, abort flag
     static constexpr int amax = misc + 16;             // fused f4_gemv: [warps][tokens] maxima
-    static constexpr size_t total = (size_t)amax + 8 * kFusedTokens * 4 + 1024;
+    static constexpr size_t total = (size_t)amax + 8 * kFusedTokens * 4;
     static_assert(used_cols <= 256, "TMEM has 512 columns, for two CTAs");
     static_assert(stage_bytes % 1024 == 0, "operand tiles start on swizzle atoms");
     static_assert(total <= kSmemTwo, "shared memory of an SM, for two CTAs");
@@ -267,9 +267,14 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     using C = Cfg<FMT, BN>;
     constexpr bool GEMV = MODE != kMm;
     constexpr bool FUSED = MODE == kGemvFused;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // Operand tiles start on 1024 bytes.  Dynamic shared memory does too (there
+    // is no static one here); slack to round its start up would cost the widest
+    // NV tile its fourth stage, so a start elsewhere is refused instead.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (w4::smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicCAS(p.err, 0, (int)W4_ERR_ALIGN);
+        return;
+    }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::bars);  // stage loaded     [stages]
     uint64_t* empty = full + C::stages;                            // stage consumed   [stages]
     uint64_t* afull = empty + C::stages;                           // tile accumulated [acc_stages]
