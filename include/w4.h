@@ -286,7 +286,8 @@ int w4a8_mmq_static(const uint8_t *codes, const uint16_t *d_f16,
  * byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
  * (r / 128) * ceil(blocks / 4) + b / 4.  Rows and blocks that pad the last
  * tiles hold 0.  f4_scale_bytes gives the plane's size.
- * R >= 0, K % 32 == 0 and K <= 131072 for every entry point below. */
+ * R >= 0, K % 32 == 0 and K <= 131072 for every entry point below.  Tensor
+ * scales are 4-byte and ids 8-byte aligned, every other pointer 16-byte. */
 typedef enum { W4_F4_MX = 0, W4_F4_NV = 1 } w4_f4_format;
 
 typedef enum { W4_IN_BF16 = 0, W4_IN_F32 = 1, W4_IN_F16 = 2 } w4_in_dtype;

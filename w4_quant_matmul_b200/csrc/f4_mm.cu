@@ -4,9 +4,10 @@
 //   f4_mm    y[t][n] = gw ga sum_k (q s)_w[n][k] (q s)_a[t][k]
 //   f4_gemv  y[t][n] = g sum_k (q s)[n][k] x[t][k],  x bf16, at most 8 tokens
 //
-// Both run one kernel.  A tile is 128 weight rows (the MMA's M, TMEM lanes) by
-// BN tokens (its N, TMEM columns); K advances in stages of 256 elements (128
-// bytes of codes a row, one 128B-swizzle atom), four MMAs of K = 64 each.
+// Both run one kernel (f4_mm of many tokens has its own: f4_pair.cu).  A tile is
+// 128 weight rows (the MMA's M, TMEM lanes) by BN tokens (its N, TMEM columns);
+// K advances in stages of 256 elements (128 bytes of codes a row, one
+// 128B-swizzle atom), four MMAs of K = 64 each.
 //   warp 0     TMA producer: the code tiles of weights and tokens and their
 //              scale tiles into a ring of shared-memory stages.
 //   warp 1     allocates TMEM; one lane copies each stage's scale tiles to TMEM
@@ -15,19 +16,26 @@
 //              run in issue order.
 //   warps 2-5  epilogue: TMEM -> registers -> y; a thread owns one weight row,
 //              so a warp's stores of one token are contiguous.
-// When the tiles do not fill the GPU, a cluster of up to 8 CTAs splits a tile's
+//   warps 6-   f4_gemv of few tokens: activation digits (below).
+// When the tiles do not fill the GPU, a cluster of up to 6 CTAs splits a tile's
 // K; each CTA leaves its fp32 partial tile in shared memory and the CTAs sum
 // them through distributed shared memory in CTA order (deterministic, and no
-// workspace).  Otherwise CTAs are persistent and the accumulators are double
-// buffered, where TMEM holds two.
+// workspace).  Otherwise CTAs are persistent and their accumulators double
+// buffered.  What bounds it: bytes from HBM for large streams, and for small
+// ones latency, of which about 4 us remain at any size: one HBM access, the MMAs'
+// completion, the sum over the cluster.  Tiles of 64 tokens at most: 128 were
+// slower wherever the CTA pairs are not faster still (2560 x 9728 at 256 tokens
+// 13.5 us against 12.6).
 //
 // f4_gemv keeps x exact to 22 bits of each block's largest magnitude without
-// leaving the 4-bit tensor cores: a first kernel writes x as fixed point in
-// eight base-8 digits -4..3, every one of them an e2m1 number, and digit j of
-// token t becomes row 8 t + j of the token operand, with the block's power of
-// two as its scale.  The epilogue sums a token's 8 columns with weights 8^-j.
-// The weights are read once, whatever the number of tokens, and no CUDA core
-// touches them.
+// leaving the 4-bit tensor cores: x is written as fixed point in eight base-8
+// digits -4..3, every one of them an e2m1 number, and digit j of token t becomes
+// row 8 t + j of the token operand, with the block's power of two as its scale.
+// The epilogue sums a token's 8 columns with weights 8^-j.  The weights are read
+// once, whatever the number of tokens, and no CUDA core touches them: at 54
+// weights a cycle and SM, unpacking them there would take most of the issue slots
+// at one token and several times too many at eight.  lm_head 151936 x 2560 (MX):
+// 31.4 us at one token, 34.7 at eight (6590 and 5950 GB/s of weights).
 #include <cuda_bf16.h>
 
 #include "f4_pair.cuh"
@@ -45,11 +53,10 @@ constexpr int kDigits = 8;      // base-8 digits of an activation
 constexpr int kMaxTokens = 8;   // f4_gemv
 constexpr int kFusedTokens = 3; // most tokens whose digits the product kernel makes itself
 
-// Tokens up to which f4_gemv is one kernel.  Against digits made by a kernel of
-// their own (us, MX at 1 / 3 / 4 tokens): 2560 x 4096 4.6 / 5.5 / 5.9 against
-// 6.4 / 6.8 / 6.8, 19456 x 2560 7.0 / 9.4 / 10.8 against 9.1 / 9.3 / 9.3,
-// 151936 x 2560 33 / 34.6 / 39.7 against 34.6 / 35.8 / 35.9.  NV looks for the
-// largest exponent first: at 3 tokens 19456 x 2560 takes 12.3 against 10.0.
+// Tokens up to which f4_gemv is one kernel.  Three tokens of MX in one (us): 2560
+// x 4096 4.9, 19456 x 2560 9.4, 2560 x 9728 7.0; four with their digits made by a
+// kernel of their own 5.7, 8.7, 7.5, and in one 5.9, 10.8, 9.0.  NV looks for the
+// largest exponent first, so it stops at two: 5.5, 10.2, 8.2 against 6.3, 9.7, 8.2.
 constexpr int fused_tokens(int fmt) { return fmt == W4_F4_MX ? 3 : 2; }
 constexpr int kMaxSplit = 6;    // CTAs of a cluster that share a tile's K
 constexpr size_t kSmemTwo = 113 * 1024;  // of each of two CTAs on an SM (228 KB, 1 KB reserved a CTA)
