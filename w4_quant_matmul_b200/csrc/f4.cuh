@@ -51,7 +51,9 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 // weights; the tensor scale: to anything but x, which the kernel before it never
 // writes -- and lets the kernel after it start once it has waited (the digit
 // kernel of f4_gemv at once).  The quantiser, which writes what f4_gemv reads
-// early, does not let the next kernel start early at all.
+// early, does not let the next kernel start early at all.  What another kernel may
+// write while this one is already there is not loaded through the read-only path
+// (__ldca, not __ldg).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

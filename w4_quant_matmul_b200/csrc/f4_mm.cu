@@ -463,12 +463,12 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         const int k_end = ke * BK < p.K ? ke * BK : p.K;
         int emax = 0;
         if constexpr (FMT == W4_F4_NV) {
-            // the largest exponent of this CTA's k, over all four warps
+            // the largest exponent of this CTA's k, over all digit warps
             volatile uint32_t* part = reinterpret_cast<volatile uint32_t*>(smem + C::amax);
             for (int tt = 0; tt < p.M; ++tt) {
                 uint32_t m = 0;
                 for (int k = kb * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
-                    m = max(m, amax8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)tt * p.K + k))));
+                    m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(p.x + (int64_t)tt * p.K + k))));
                 m = __reduce_max_sync(0xffffffffu, m);
                 if (lane == 0) part[w * kFusedTokens + tt] = m;
             }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         auto load_x = [&](int i) {
             const int k = (kb + i % stages) * BK + lane * 8;
             if (i < total && k < p.K && W4_CHECK(k + 8 <= p.K && t < p.M, p.err))
-                return __ldg(reinterpret_cast<const uint4*>(xt + k));
+                return __ldca(reinterpret_cast<const uint4*>(xt + k));
             return make_uint4(0u, 0u, 0u, 0u);
         };
         if (turn < per) {  // (three tokens may leave a warp without work)
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         float alpha = 1.0f;
         float* part = reinterpret_cast<float*>(smem);  // split K: [column][128] in the ring
         pdl_wait();
-        if constexpr (FMT == W4_F4_NV) alpha = GEMV ? __ldg(p.gw) : __fmul_rn(__ldg(p.gw), __ldg(p.ga));
+        if constexpr (FMT == W4_F4_NV) alpha = GEMV ? __ldca(p.gw) : __fmul_rn(__ldca(p.gw), __ldca(p.ga));
         if constexpr (FUSED && FMT == W4_F4_NV) digit_barrier<BN>();
         // NV: the factor that the digits of token t leave out
         auto factor = [&](int t) {
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                 for (int i = 0; i < digit_warps(BN); ++i) m = max(m, part[i * kFusedTokens + t]);
                 return nv_factor(exp_field(m));
             } else {
-                return __ldg(p.row_factor + t);
+                return __ldca(p.row_factor + t);
             }
         };
         int ti = 0;
@@ -604,11 +604,11 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
             const int row = lane * 4, n = tn * BM + row;  // four weight rows a thread
             const int cols = p.M - t0 < BN ? p.M - t0 : BN;
             float alpha = 1.0f;
-            if constexpr (FMT == W4_F4_NV && !GEMV) alpha = __fmul_rn(__ldg(p.gw), __ldg(p.ga));
+            if constexpr (FMT == W4_F4_NV && !GEMV) alpha = __fmul_rn(__ldca(p.gw), __ldca(p.ga));
             const uint32_t base = w4::smem_u32(smem) + row * 4;
             // columns split, split + splits, ...: one a warp and step, two steps'
             // loads in flight
-            const int cstep = p.splits * (kEpiWarps);
+            const int cstep = p.splits * kEpiWarps;
 #pragma unroll 1
             for (int c = split + p.splits * (warp - kEpiWarp0); c < cols; c += 2 * cstep) {
                 float4 v[2][kMaxSplit];
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kDigitThreads)
         __shared__ uint32_t part[kDigitThreads / 32];
         uint32_t m = 0;
         for (int k = threadIdx.x * 8; k < K; k += kDigitElems)
-            m = max(m, amax8(__ldg(reinterpret_cast<const uint4*>(xt + k))));
+            m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(xt + k))));
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kDigitThreads)
     if (k - lane * 8 >= kpad) return;
     const bool live = k < K;
     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (live && W4_CHECK(k + 8 <= K, err)) raw = __ldg(reinterpret_cast<const uint4*>(xt + k));
+    if (live && W4_CHECK(k + 8 <= K, err)) raw = __ldca(reinterpret_cast<const uint4*>(xt + k));
     uint32_t out[kDigits], word;
     digits8<FMT>(raw, live, emax, lane, out, word);
     if (live) {

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         uint8_t* st = smem + C::out + (warp - 2) * 32 * kChunk * 4;
         pdl_wait();
-        const float alpha = FMT == W4_F4_NV ? __fmul_rn(__ldg(p.gw), __ldg(p.ga)) : 1.0f;
+        const float alpha = FMT == W4_F4_NV ? __fmul_rn(__ldca(p.gw), __ldca(p.ga)) : 1.0f;
         const bool aligned = p.N % vec == 0;  // rows of y start on 16 bytes
         int ti = 0;
         for (int tile = first; tile < tiles; tile += step, ++ti) {

@@ -37,10 +37,10 @@ __device__ __forceinline__ Raw8<IN> load8(const void* x, int64_t elem) {
     Raw8<IN> r;
     if constexpr (IN == W4_IN_F32) {
         const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + elem);
-        r.a = __ldg(s);
-        r.b = __ldg(s + 1);
+        r.a = __ldca(s);
+        r.b = __ldca(s + 1);
     } else {
-        r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + elem));
+        r.a = __ldca(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + elem));
     }
     return r;
 }
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
                 raw[u][o] = load8<IN>(x, r * K + k + 8 * o);
         }
     }
-    const float g = FMT == W4_F4_NV ? __ldg(gp) : 1.0f;
+    const float g = FMT == W4_F4_NV ? __ldca(gp) : 1.0f;
     const float g6 = __fmul_rn(6.0f, g), rcp = __frcp_rn(g6);
     uint8_t* code_row = codes + r * (K / 2);
     uint8_t* scale_row = scales + f4::scale_word(r, 0, tiles_k);
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads)
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= T) return;
-    const int64_t row = LOOKUP ? __ldg(ids + t) : t;
+    const int64_t row = LOOKUP ? __ldca(ids + t) : t;
     const bool live = row >= 0 && row < V;
     const uint8_t* code_row = codes + row * (K / 2);
     const uint8_t* scale_row = scales + f4::scale_word(row, 0, f4::scale_tiles_k(K, FMT));
@@ -342,14 +342,14 @@ __global__ void __launch_bounds__(kThreads)
         if (live && k < K && W4_CHECK(k + kElems <= K, err)) {
             const uint8_t* c = code_row + k / 2;
             if constexpr (kElems == 8)
-                q[u] = __ldg(reinterpret_cast<const uint32_t*>(c));
+                q[u] = __ldca(reinterpret_cast<const uint32_t*>(c));
             else
-                q[u] = __ldg(reinterpret_cast<const uint16_t*>(c));
+                q[u] = __ldca(reinterpret_cast<const uint16_t*>(c));
             const int b = k / f4::block_of(FMT);
-            sb[u] = __ldg(scale_row + (b >> 2) * f4::kTileBytes + (b & 3));
+            sb[u] = __ldca(scale_row + (b >> 2) * f4::kTileBytes + (b & 3));
         }
     }
-    const float c = FMT == W4_F4_NV ? __fmul_rn(__ldg(gp), alpha) : alpha;
+    const float c = FMT == W4_F4_NV ? __fmul_rn(__ldca(gp), alpha) : alpha;
 #pragma unroll
     for (int u = 0; u < kSegs; ++u) {
         const int k = k0 + u * kSpan;
