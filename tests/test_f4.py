@@ -531,6 +531,38 @@ def test_weights_written_just_before(torch, w4):
         assert torch.equal(y, again)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_large_weights_written_just_before(torch, w4, fmt):
+    """The same for streams of several tiles a CTA, whose first weights are
+    requested before the kernel ahead has completed: planes that the quantiser or
+    a copy on the stream has just written, directly ahead of the product."""
+    N, K = 40000, 512
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    srcs = [torch.randn(N, K, device="cuda", generator=gen) for _ in range(2)]
+    sets = [w4.f4_quantize(s, fmt) for s in srcs]
+    for M in (1, 5):
+        x = dev(torch, activations(M, K, 73)).bfloat16()
+        torch.cuda.synchronize()
+        want = []
+        for p in sets:
+            want.append(w4.f4_gemv(*p, x))
+            torch.cuda.synchronize()
+        codes, scales = (torch.empty_like(t) for t in sets[0][:2])
+        y = torch.empty_like(want[0])
+        for i in range(12):
+            k, g = i % 2, sets[i % 2][2]
+            y.fill_(float("nan"))
+            w4.f4_gemv(*sets[1 - k], x)      # a kernel that lets the next start early
+            if i % 4 < 2:
+                w4.f4_quantize(srcs[k], fmt, g, codes, scales)
+            else:
+                codes.copy_(sets[k][0])
+                scales.copy_(sets[k][1])
+            w4.f4_gemv(codes, scales, g, x, y=y)
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[k]), (M, i)
+
+
 def test_workspace_too_small_is_refused(torch, w4):
     w = random_matrix(torch, 64, 96, "mx", 81)
     x = dev(torch, activations(5, 96, 82)).bfloat16()

@@ -3,11 +3,13 @@
 //
 // All four move bytes and nothing else: the quantiser reads 2 or 4 bytes and
 // writes 0.53 (MX) or 0.56 (NV) per element, the other way round for the
-// dequantiser.  A lane owns 8 consecutive elements, so that a warp's loads and
-// code stores are contiguous (128 bytes of codes, 512 or 1024 of elements);
-// the lanes of a block (4 for MX, 2 for NV) find its largest magnitude with
-// shuffles, and the lanes of 4 blocks join their scale bytes into the one
-// 4-byte word that the scale tile holds for them.
+// dequantiser.  A lane owns 8 (NV: 16) consecutive elements, so that a warp's
+// loads and code stores are contiguous; the lanes of a block find its largest
+// magnitude with shuffles (4 lanes for MX, one for NV), and the lanes of 4 blocks
+// join their scale bytes into the one 4-byte word that the scale tile holds for
+// them.  HBM bounds them: 8192 x 9728 bf16 quantised in 33.4 us (MX, 6020 GB/s) and
+// 35.2 (NV, 5730), turned back into bf16 in 33.8 (5970) and into fp32 in 60.6
+// (5950); their scale found in 26.2 (6070).
 #include <cuda_bf16.h>
 
 #include "f4.cuh"
