@@ -563,6 +563,40 @@ def test_large_weights_written_just_before(torch, w4, fmt):
             assert torch.equal(y, want[k]), (M, i)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_weights_from_another_stream(torch, w4, fmt):
+    """Planes and activations written late on one stream, an event, the product on
+    another stream behind kernels that let it start early."""
+    N, K = 40000, 512
+    gen = torch.Generator(device="cuda").manual_seed(19)
+    src = [torch.randn(N, K, device="cuda", generator=gen) for _ in range(2)]
+    sets = [w4.f4_quantize(s, fmt) for s in src]
+    xs = [dev(torch, activations(5, K, 80 + i)).bfloat16() for i in range(2)]
+    torch.cuda.synchronize()
+    want = {}
+    for k in range(2):
+        for m in (1, 5):
+            want[k, m] = w4.f4_gemv(*sets[k], xs[k][:m])
+    codes, scales, x = (t.clone() for t in (*sets[0][:2], xs[0]))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(6):
+        k = i % 2
+        with torch.cuda.stream(a):
+            torch.cuda._sleep(2_000_000)
+            w4.f4_quantize(src[k], fmt, sets[k][2], codes, scales)
+            x.copy_(xs[k])
+            done = a.record_event()
+        with torch.cuda.stream(b):
+            w4.f4_gemv(*sets[0], xs[0])
+            b.wait_event(done)
+            got = {m: w4.f4_gemv(codes, scales, sets[k][2], x[:m]) for m in (1, 5)}
+            a.wait_stream(b)
+        torch.cuda.synchronize()
+        for m in (1, 5):
+            assert torch.equal(got[m], want[k, m]), (i, m)
+
+
 def test_workspace_too_small_is_refused(torch, w4):
     w = random_matrix(torch, 64, 96, "mx", 81)
     x = dev(torch, activations(5, 96, 82)).bfloat16()
