@@ -267,6 +267,31 @@ def test_gemv(torch, w4, fmt, N, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiles,K", [(296, 512), (297, 512), (297, 1056), (310, 2592), (345, 2592),
+                                     (405, 1312), (590, 1056), (593, 1056)])
+def test_gemv_of_one_to_two_tiles_a_cta(torch, w4, fmt, tiles, K):
+    """Row counts about one and two times the CTAs that run at once, where tiles
+    may be left over for clusters: 13 row tiles (1664 rows) over and over, so that
+    any mix-up of tiles shows, and a last one that ends early."""
+    base = random_matrix(torch, 13 * 128, K, fmt, seed=K)
+    N = tiles * 128 - 37
+    reps = -(-tiles // 13)
+    codes = base.planes[0].repeat(reps, 1)[:N].contiguous()
+    plane = base.planes[1].repeat(reps, 1, 1)[:tiles].contiguous()
+    for M in (1, 2, 3, 4, 5, 8):
+        x = dev(torch, activations(M, K, seed=M)).bfloat16()
+        x64 = host(x.double())
+        room = torch.full((M * N + 64,), 7.0, device="cuda")
+        y = room[:M * N].view(M, N)
+        w4.f4_gemv(codes, plane, base.planes[2], x, y=y)
+        y16 = w4.f4_gemv(codes, plane, base.planes[2], x)
+        assert (room[M * N:] == 7.0).all()
+        every = lambda a: np.tile(a, (1, reps))[:, :N]
+        check_product(torch, y, y16, every(x64 @ base.scaled.T),
+                      every(ref.gemv_bound(x64, base.scaled, K, fmt)))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_gemv_is_exact_for_small_integers(torch, w4, fmt):
     # integer weights and activations whose sums stay below 2^24: every fp32
     # partial sum is an integer, so the result has no error at all

@@ -21,7 +21,8 @@
 // K; each CTA leaves its fp32 partial tile in shared memory and the CTAs sum
 // them through distributed shared memory in CTA order (deterministic, and no
 // workspace).  Otherwise CTAs are persistent and their accumulators double
-// buffered.  What bounds it: bytes from HBM for large streams, and for small
+// buffered; f4_gemv, where they would take one or two tiles each, takes one and
+// splits the others' K so.  What bounds it: bytes from HBM for large streams, and for small
 // ones latency, of which about 4 us remain at any size: one HBM access, the MMAs'
 // completion, the sum over the cluster.  Tiles of 64 tokens at most: 128 were
 // slower wherever the CTA pairs are not faster still (2560 x 9728 at 256 tokens
@@ -111,7 +112,8 @@ struct Params {
     int stages_k;      // ceil(K / BK)
     int tiles_k;       // scale tiles along K
     int tiles_n, tiles_m;
-    int splits;
+    int whole;         // tiles that each CTA takes in whole, before
+    int splits;        // the CTAs of a cluster share one along K
     int out_f32;
     int* err;
 };
@@ -261,6 +263,15 @@ constexpr int threads_of(int bn, Mode mode) {
     return 32 * (kDigitWarp0 + (mode == kGemvFused ? digit_warps(bn) : 0));
 }
 
+// CTAs an SM for the register allocation.  Two run there in any case; asking for
+// them lets the compiler take more registers, and the loads of the sum over a
+// cluster overlap (2560 x 4096, MX and NV, 4 tokens: 5.87 -> 5.63, 6.85 -> 6.53
+// us).  The digits of MX at one and two tokens are slower for it (2560 x 9728:
+// 5.89 -> 6.70).
+constexpr int min_ctas(int fmt, int bn, Mode mode) {
+    return mode == kGemvFused && fmt == W4_F4_MX && bn == 16 ? 0 : 2;
+}
+
 // Digit and epilogue warps meet: the maxima of the tokens are in shared memory.
 template <int BN>
 __device__ __forceinline__ void digit_barrier() {
@@ -268,7 +279,7 @@ __device__ __forceinline__ void digit_barrier() {
 }
 
 template <int FMT, int BN, Mode MODE>
-__global__ void __launch_bounds__(threads_of(BN, MODE))
+__global__ void __launch_bounds__(threads_of(BN, MODE), min_ctas(FMT, BN, MODE))
     f4_mm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const Params p) {
     using C = Cfg<FMT, BN>;
@@ -294,10 +305,16 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     const int lane = threadIdx.x & 31;
     const int tiles = p.tiles_n * p.tiles_m;
     const int split = p.splits > 1 ? (int)cluster_rank() : 0;
-    const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
-    // this CTA's stages of every tile
+    // unit u of this CTA: a whole tile, at the end its K slice of the cluster's
+    const int shared = p.whole * gridDim.x + blockIdx.x / p.splits;
+    const int units = p.whole + (shared < tiles ? 1 : 0);
     const int kb = (int)((int64_t)p.stages_k * split / p.splits);
     const int ke = (int)((int64_t)p.stages_k * (split + 1) / p.splits);
+    auto tile_of = [&](int u) {
+        return u < p.whole ? u * (int)gridDim.x + (int)blockIdx.x : shared;
+    };
+    auto k_from = [&](int u) { return u < p.whole ? 0 : kb; };
+    auto k_to = [&](int u) { return u < p.whole ? p.stages_k : ke; };
 
     const int chunks_last = p.tiles_k - (p.stages_k - 1) * C::chunks;
     auto chunks_of = [&](int ks) { return ks + 1 < p.stages_k ? C::chunks : chunks_last; };
@@ -331,8 +348,10 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     // still has to load.
     int pre = 0;
     if constexpr (GEMV)
-        if (first < tiles && (!FUSED || many_tiles(tiles, gridDim.x)))
-            pre = ke - kb < C::stages ? ke - kb : C::stages;
+        if (units > 0 && (!FUSED || many_tiles(tiles, gridDim.x))) {
+            pre = k_to(0) - k_from(0);
+            if (pre > C::stages) pre = C::stages;
+        }
 
     if (threadIdx.x == 0) {
         w4::prefetch_tmap(&tm_a);
@@ -349,7 +368,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         w4::mbar_init(drain, 1);
         *abort_flag = 0;
         w4::fence_mbar_init();
-        for (int i = 0; i < pre; ++i) load_a(i, kb + i, first);
+        for (int i = 0; i < pre; ++i) load_a(i, k_from(0) + i, tile_of(0));
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -378,11 +397,12 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
             bool ok = true;
             pdl_wait();
             pdl_trigger();
-            for (int tile = first; tile < tiles && ok; tile += step) {
+            for (int u = 0; u < units && ok; ++u) {
+                const int tile = tile_of(u), k0 = k_from(u), k1 = k_to(u);
                 const int tn = GEMV ? tile : tile / p.tiles_m;
                 const int tm = GEMV ? 0 : tile % p.tiles_m;
-                (void)W4_CHECK(tn < p.tiles_n && tm < p.tiles_m && kb < ke, p.err);
-                for (int ks = kb; ks < ke; ++ks, ++it) {
+                (void)W4_CHECK(tn < p.tiles_n && tm < p.tiles_m && k0 < k1, p.err);
+                for (int ks = k0; ks < k1; ++ks, ++it) {
                     const int s = it % C::stages;
                     if (it >= pre) {
                         if (!w4::mbar_wait(&empty[s], ((uint32_t)(it / C::stages) & 1u) ^ 1u,
@@ -403,20 +423,21 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         // ---------------- MMA issuer ----------------
         if (w4::elect_one()) {
             const uint32_t sf0 = tmem + C::acc_stages * C::acc_cols;
-            int it = 0, ti = 0;
+            int it = 0;
             bool ok = true;
-            for (int tile = first; tile < tiles && ok; tile += step, ++ti) {
+            for (int ti = 0; ti < units && ok; ++ti) {
+                const int k0 = k_from(ti), k1 = k_to(ti);
                 // an odd 64-token tile starts in the middle of its 128-row scale
                 // tile, at TMEM column 2 (32 rows a column; scale addresses must
                 // be even, so narrower tiles come one to a product)
-                const uint32_t sb_col = !GEMV && BN == 64 ? (uint32_t)(tile % p.tiles_m & 1) * 2 : 0u;
+                const uint32_t sb_col = !GEMV && BN == 64 ? (uint32_t)(tile_of(ti) % p.tiles_m & 1) * 2 : 0u;
                 const int as = ti % C::acc_stages;
                 const uint32_t d = tmem + as * C::acc_cols;
                 if (!w4::mbar_wait(&aempty[as], ((uint32_t)(ti / C::acc_stages) & 1u) ^ 1u,
                                    abort_flag, p.err))
                     break;
                 tc_fence_after();
-                for (int ks = kb; ks < ke; ++ks, ++it) {
+                for (int ks = k0; ks < k1; ++ks, ++it) {
                     const int s = it % C::stages;
                     if (!w4::mbar_wait(&full[s], (uint32_t)(it / C::stages) & 1u, abort_flag,
                                        p.err)) {
@@ -446,7 +467,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                         mma_f4<FMT>(d, operand_desc(a + j * (kMmaK / 2)),
                                     operand_desc(b + j * (kMmaK / 2)), instr_desc<FMT, BM, BN>(id),
                                     sf + c * 4, sfb + c * 4 + sb_col,
-                                    ks > kb || j > 0);
+                                    ks > k0 || j > 0);
                     }
                     mma_commit(&empty[s]);
                 }
@@ -468,14 +489,15 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         constexpr int kWordLanes = block_of(FMT) / 2;
         pdl_wait();
         const uint16_t* xt = p.x + (int64_t)t * p.K;
-        const int k_end = ke * BK < p.K ? ke * BK : p.K;
+        const int k_end = k_to(0) * BK < p.K ? k_to(0) * BK : p.K;
         int emax = 0;
         if constexpr (FMT == W4_F4_NV) {
-            // the largest exponent of this CTA's k, over all digit warps
+            // the largest exponent of this CTA's k (its first tile's hold the
+            // others'), over all digit warps
             volatile uint32_t* part = reinterpret_cast<volatile uint32_t*>(smem + C::amax);
             for (int tt = 0; tt < p.M; ++tt) {
                 uint32_t m = 0;
-                for (int k = kb * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
+                for (int k = k_from(0) * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
                     m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(p.x + (int64_t)tt * p.K + k))));
                 m = __reduce_max_sync(0xffffffffu, m);
                 if (lane == 0) part[w * kFusedTokens + tt] = m;
@@ -488,20 +510,27 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
         }
         // the activations of the warp's next stage are loaded before it works on
         // the present one; the stages of one tile follow those of the tile before
-        const int stages = ke - kb;
-        const int total = first < tiles ? ((tiles - 1 - first) / step + 1) * stages : 0;
-        auto load_x = [&](int i) {
-            const int k = (kb + i % stages) * BK + lane * 8;
+        const int total = p.whole * p.stages_k + (shared < tiles ? ke - kb : 0);
+        // a tile's last stage is followed by the next one's first: kb, which is
+        // 0 unless a shared tile follows the only whole one
+        auto wrap = [&](int ks) {
+            while (ks >= p.stages_k) ks += kb - p.stages_k;
+            return ks;
+        };
+        auto load_x = [&](int i, int ks) {
+            const int k = ks * BK + lane * 8;
             if (i < total && k < p.K && W4_CHECK(k + 8 <= p.K && t < p.M, p.err))
                 return __ldca(reinterpret_cast<const uint4*>(xt + k));
             return make_uint4(0u, 0u, 0u, 0u);
         };
         if (turn < per) {  // (three tokens may leave a warp without work)
-            uint4 next = load_x(turn);
+            int ks_next = wrap(k_from(0) + turn);
+            uint4 next = load_x(turn, ks_next);
             for (int it = turn; it < total; it += per) {
                 const uint4 raw = next;
-                next = load_x(it + per);
-                const bool live = (kb + it % stages) * BK + lane * 8 < p.K;
+                const bool live = ks_next * BK + lane * 8 < p.K;
+                ks_next = wrap(ks_next + per);
+                next = load_x(it + per, ks_next);
                 uint32_t out[kDigits], word;
                 digits8<FMT>(raw, live, emax, lane, out, word);
                 const int s = it % C::stages;
@@ -544,8 +573,9 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                 return __ldca(p.row_factor + t);
             }
         };
-        int ti = 0;
-        for (int tile = first; tile < tiles; tile += step, ++ti) {
+        for (int ti = 0; ti < units; ++ti) {
+            const int tile = tile_of(ti);
+            const bool partial = p.splits > 1 && (!GEMV || ti == p.whole);
             const int tn = GEMV ? tile : tile / p.tiles_m;
             const int tm = GEMV ? 0 : tile % p.tiles_m;
             const int as = ti % C::acc_stages;
@@ -571,7 +601,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
                         if (t < p.M) {
                             // (one at a time: their product could leave the range of fp32)
                             if constexpr (FMT == W4_F4_NV) v = v * factor(t) * alpha;
-                            if (p.splits > 1)
+                            if (partial)
                                 part[t * BM + row] = v;
                             else if (n < p.N)
                                 store_y(p, t, n, v);
@@ -589,7 +619,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float v = __uint_as_float(r[i]);
-                        if (p.splits > 1)
+                        if (partial)
                             part[(c + i) * BM + row] = v;
                         else if (t0 + i < p.M && n < p.N)
                             store_y(p, t0 + i, n, v * alpha);
@@ -603,12 +633,12 @@ __global__ void __launch_bounds__(threads_of(BN, MODE))
     }
 
     if (p.splits > 1) {
-        // one tile per cluster: the partial tiles, summed in CTA order; the
+        // the cluster's tile: the partial tiles, summed in CTA order; the
         // columns are dealt out to the CTAs
         cluster_sync();
-        if (warp >= kEpiWarp0 && warp < kDigitWarp0 && !*abort_flag) {
-            const int tn = GEMV ? first : first / p.tiles_m;
-            const int t0 = GEMV ? 0 : first % p.tiles_m * BN;
+        if (warp >= kEpiWarp0 && warp < kDigitWarp0 && shared < tiles && !*abort_flag) {
+            const int tn = GEMV ? shared : shared / p.tiles_m;
+            const int t0 = GEMV ? 0 : shared % p.tiles_m * BN;
             const int row = lane * 4, n = tn * BM + row;  // four weight rows a thread
             const int cols = p.M - t0 < BN ? p.M - t0 : BN;
             float alpha = 1.0f;
@@ -765,29 +795,63 @@ int launch_tiles(const uint8_t* codes, const uint8_t* bcodes, Params p, cudaStre
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    // CTAs along K of each tile: as many as still run all at once, with at
-    // least two stages each
-    p.splits = 1;
-    for (int s = kMaxSplit; s > 1; --s) {
-        if (p.stages_k / s < 2 || tiles * s > 2 * (int64_t)w4::sm_count()) continue;
+    // CTAs of clusters of s that run at once
+    auto cluster_slots = [&](int s, int64_t* ctas) {
         if (clusters[s] == 0) {
             attr[0].val.clusterDim.x = (unsigned)s;
             cfg.gridDim = dim3((unsigned)s);
             cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&clusters[s], kernel, &cfg);
-            if (e != cudaSuccess) return w4::cuda_fail(e);
+            const cudaError_t err = cudaOccupancyMaxActiveClusters(&clusters[s], kernel, &cfg);
+            if (err != cudaSuccess) return err;
             if (clusters[s] == 0) clusters[s] = -1;  // asked, none
         }
         // the query counts one CTA an SM where two run: 48 tiles still start at
         // once in clusters of 5 (26 by the query) and no longer in 6 (22), 80 in
         // 3 (45) and not in 4 (33), each step too far costing half as much again
-        if (tiles <= 2 * clusters[s]) {
-            p.splits = s;
-            break;
+        *ctas = clusters[s] > 0 ? (int64_t)clusters[s] * 2 * s : 0;
+        return cudaSuccess;
+    };
+    const int64_t slots = (int64_t)w4::sm_count() * 2;
+    int64_t grid = tiles < slots ? tiles : slots;
+    p.splits = 1;
+    p.whole = (int)(tiles / grid);
+    if (!many_tiles(tiles, slots)) {
+        // CTAs along K of each tile: as many as still run all at once, with at
+        // least two stages each
+        for (int s = kMaxSplit; s > 1; --s) {
+            int64_t ctas;
+            if (p.stages_k / s < 2 || tiles * s > slots) continue;
+            if ((e = cluster_slots(s, &ctas)) != cudaSuccess) return w4::cuda_fail(e);
+            if (tiles * s <= ctas) {
+                p.splits = s;
+                p.whole = 0;
+                grid = tiles * s;
+                break;
+            }
+        }
+    } else if (MODE != kMm && tiles < 2 * slots) {
+        // f4_gemv: one whole tile each, and clusters for what is left over, of
+        // the size that ends soonest (us at one and eight tokens: 40000 x 8192
+        // MX 33.8 -> 29.0 and 37.4 -> 32.1, NV 38.2 -> 31.3 and 44.6 -> 35.4;
+        // 50304 x 4096 MX 20.9 -> 19.7).  In longer streams the CTAs drift apart
+        // and fill the end by themselves, and clusters leave slots empty: 128256
+        // x 2560 was 26.7 -> 28.4.  f4_mm gained nothing (50304 x 4096 at 16
+        // tokens 21.2, 21.1), and its narrow streams lost by the longer code.
+        int64_t best = 2 * 60;  // two tiles' time, in 60ths of a tile's
+        for (int s = 2; s <= kMaxSplit; ++s) {
+            int64_t ctas;
+            if (p.stages_k / s < 2) break;
+            if ((e = cluster_slots(s, &ctas)) != cudaSuccess) return w4::cuda_fail(e);
+            if (ctas == 0) continue;
+            const int64_t rest = tiles % ctas, t = 60 * (tiles / ctas) + (rest > 0 ? 60 / s : 0);
+            if (rest * s <= ctas && t < best) {
+                best = t;
+                p.splits = s;
+                p.whole = (int)(tiles / ctas);
+                grid = ctas;
+            }
         }
     }
-    const int64_t slots = (int64_t)w4::sm_count() * 2;
-    const int64_t grid = p.splits > 1 ? tiles * p.splits : (tiles < slots ? tiles : slots);
     attr[0].val.clusterDim.x = (unsigned)p.splits;
     cfg.gridDim = dim3((unsigned)grid);
     cfg.numAttrs = 2;
