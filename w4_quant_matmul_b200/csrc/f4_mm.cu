@@ -211,29 +211,29 @@ __device__ __forceinline__ void digits8(const uint4& raw, bool live, int emax, i
     for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
         word |= __shfl_xor_sync(0xffffffffu, word, off);
 
+    // v = x * 2^(21 - E) rounded to an integer (ties to even): added to 3 * 2^22 it
+    // is the low bits of the sum.  In two factors, as the power itself leaves the
+    // range of fp32 for the smallest E; the first is exact.  (A bad block's digits
+    // may be any: its scale is NaN.)
+    const float up = eb < 64 ? 0x1p64f : 1.0f;
+    const float to_int = __uint_as_float((uint32_t)(eb < 64 ? 275 - 64 - eb : 275 - eb) << 23);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t lo[4], hi[4];  // codes of digits 7..4 and 3..0, a byte each, by pair of elements
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t h = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-        const int e = exp_field(h);
-        const uint32_t mant = (h & 0x7Fu) | ((h & 0x7F80u) ? 0x80u : 0u);
-        // x = +-mant * 2^(e - 134); v = x * 2^(21 - E) = +-mant * 2^(14 - (eb - e)),
-        // rounded half up in magnitude
-        const int right = eb - e - 14;
-        uint32_t v = right <= 0 ? mant << -right
-                                : (right < 10 ? (mant + (1u << (right - 1))) >> right : 0u);
-        if (bad) v = 0u;
-        uint32_t u = (h & 0x8000u ? 0u - v : v) + 9586980u;  // 4 (8^8 - 1) / 7
-        // octal digits to nibbles, then each to its e2m1 code by table
-        u = (u & 0x00000FFFu) | ((u & 0x00FFF000u) << 4);
-        u = (u & 0x003F003Fu) | ((u & 0x0FC00FC0u) << 2);
-        u = (u & 0x07070707u) | ((u & 0x38383838u) << 1);
+        const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        uint32_t u = __float_as_uint(fmaf(x * up, to_int, 12582912.0f));
+        u += 9586980u - 0x4B400000u;  // v + 4 (8^8 - 1) / 7
+        // octal digits to nibbles (a field moves up n bits by 2^n - 1 times itself),
+        // then each to its e2m1 code by table
+        u += (u & 0x00FFF000u) * 15u;
+        u += (u & 0x0FC00FC0u) * 3u;
+        u += u & 0x38383838u;
         // -4 -3 -2 -1 | 0 1 2 3
         const uint32_t a = __byte_perm(0x0A0C0D0Eu, 0x05040200u, u);
         const uint32_t b = __byte_perm(0x0A0C0D0Eu, 0x05040200u, u >> 16);
-        lo[i / 2] = i & 1 ? lo[i / 2] | a << 4 : a;
-        hi[i / 2] = i & 1 ? hi[i / 2] | b << 4 : b;
+        lo[i / 2] = i & 1 ? lo[i / 2] + (a << 4) : a;
+        hi[i / 2] = i & 1 ? hi[i / 2] + (b << 4) : b;
     }
     // byte i of the four pairs -> one word
 #pragma unroll
@@ -252,8 +252,8 @@ __device__ __forceinline__ void digits8(const uint4& raw, bool live, int emax, i
 // kernel
 // ---------------------------------------------------------------------------
 
-// Digit warps of the fused f4_gemv: a warp takes about 1300 cycles for a token's
-// stage, which one SM's share of HBM delivers every 850.
+// Digit warps of the fused f4_gemv.  A CTA's share of HBM delivers a stage about
+// every 900 cycles, which two warps a token keep up with.
 constexpr int digit_warps(int bn) { return bn / kDigits * 2; }
 
 // Whether CTAs of a grid without K slices work on several tiles each.
@@ -263,23 +263,17 @@ constexpr int threads_of(int bn, Mode mode) {
     return 32 * (kDigitWarp0 + (mode == kGemvFused ? digit_warps(bn) : 0));
 }
 
-// CTAs an SM for the register allocation.  Two run there in any case; asking for
-// them lets the compiler take more registers, and the loads of the sum over a
-// cluster overlap (2560 x 4096, MX and NV, 4 tokens: 5.87 -> 5.63, 6.85 -> 6.53
-// us).  The digits of MX at one and two tokens are slower for it (2560 x 9728:
-// 5.89 -> 6.70).
-constexpr int min_ctas(int fmt, int bn, Mode mode) {
-    return mode == kGemvFused && fmt == W4_F4_MX && bn == 16 ? 0 : 2;
-}
-
 // Digit and epilogue warps meet: the maxima of the tokens are in shared memory.
 template <int BN>
 __device__ __forceinline__ void digit_barrier() {
     asm volatile("bar.sync 1, %0;" ::"n"(32 * (kEpiWarps + digit_warps(BN))) : "memory");
 }
 
+// Two CTAs run on an SM in any case; asking for them lets the compiler take more
+// registers, and the loads of the sum over a cluster overlap (2560 x 4096 at 4
+// tokens, MX and NV: 5.87 -> 5.63, 6.85 -> 6.53 us).
 template <int FMT, int BN, Mode MODE>
-__global__ void __launch_bounds__(threads_of(BN, MODE), min_ctas(FMT, BN, MODE))
+__global__ void __launch_bounds__(threads_of(BN, MODE), 2)
     f4_mm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const Params p) {
     using C = Cfg<FMT, BN>;
