@@ -258,7 +258,7 @@ def activations(M, K, seed):
 @pytest.mark.parametrize("N,K", GEMV_SHAPES)
 def test_gemv(torch, w4, fmt, N, K):
     w = random_matrix(torch, N, K, fmt, seed=N + K)
-    for M in (range(1, 9) if N * K < 2 ** 21 else (1, 3, 8)):
+    for M in range(1, 9):
         x = dev(torch, activations(M, K, seed=M + K)).bfloat16()
         x64 = host(x.double())
         y = w4.f4_gemv(*w.planes, x, out_dtype=torch.float32)
@@ -278,7 +278,7 @@ def test_gemv_of_one_to_two_tiles_a_cta(torch, w4, fmt, tiles, K):
     reps = -(-tiles // 13)
     codes = base.planes[0].repeat(reps, 1)[:N].contiguous()
     plane = base.planes[1].repeat(reps, 1, 1)[:tiles].contiguous()
-    for M in (1, 2, 3, 4, 5, 8):
+    for M in (1, 2, 3, 4, 5, 6, 8):
         x = dev(torch, activations(M, K, seed=M)).bfloat16()
         x64 = host(x.double())
         room = torch.full((M * N + 64,), 7.0, device="cuda")
@@ -531,9 +531,9 @@ def test_outputs_stay_inside(torch, w4):
 
 def test_workspace_contents_do_not_matter(torch, w4):
     for fmt in FORMATS:
-        w = random_matrix(torch, 200, 288, fmt, 61)
-        x = dev(torch, activations(5, 288, 62)).bfloat16()
-        need = w4.f4_gemv_workspace_size(5, 200, 288, fmt)
+        w = random_matrix(torch, 6500, 288, fmt, 61)
+        x = dev(torch, activations(7, 288, 62)).bfloat16()
+        need = w4.f4_gemv_workspace_size(7, 6500, 288, fmt)
         outs = []
         for fill in (0x00, 0xFF, 0x7F):
             ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
@@ -565,7 +565,7 @@ def test_large_weights_written_just_before(torch, w4, fmt):
     gen = torch.Generator(device="cuda").manual_seed(9)
     srcs = [torch.randn(N, K, device="cuda", generator=gen) for _ in range(2)]
     sets = [w4.f4_quantize(s, fmt) for s in srcs]
-    for M in (1, 5):
+    for M in (1, 5, 7):
         x = dev(torch, activations(M, K, 73)).bfloat16()
         torch.cuda.synchronize()
         want = []
@@ -596,11 +596,11 @@ def test_weights_from_another_stream(torch, w4, fmt):
     gen = torch.Generator(device="cuda").manual_seed(19)
     src = [torch.randn(N, K, device="cuda", generator=gen) for _ in range(2)]
     sets = [w4.f4_quantize(s, fmt) for s in src]
-    xs = [dev(torch, activations(5, K, 80 + i)).bfloat16() for i in range(2)]
+    xs = [dev(torch, activations(7, K, 80 + i)).bfloat16() for i in range(2)]
     torch.cuda.synchronize()
     want = {}
     for k in range(2):
-        for m in (1, 5):
+        for m in (1, 5, 7):
             want[k, m] = w4.f4_gemv(*sets[k], xs[k][:m])
     codes, scales, x = (t.clone() for t in (*sets[0][:2], xs[0]))
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
@@ -615,18 +615,18 @@ def test_weights_from_another_stream(torch, w4, fmt):
         with torch.cuda.stream(b):
             w4.f4_gemv(*sets[0], xs[0])
             b.wait_event(done)
-            got = {m: w4.f4_gemv(codes, scales, sets[k][2], x[:m]) for m in (1, 5)}
+            got = {m: w4.f4_gemv(codes, scales, sets[k][2], x[:m]) for m in (1, 5, 7)}
             a.wait_stream(b)
         torch.cuda.synchronize()
-        for m in (1, 5):
+        for m in (1, 5, 7):
             assert torch.equal(got[m], want[k, m]), (i, m)
 
 
 def test_workspace_too_small_is_refused(torch, w4):
     w = random_matrix(torch, 64, 96, "mx", 81)
-    x = dev(torch, activations(5, 96, 82)).bfloat16()
-    need = w4.f4_gemv_workspace_size(5, 64, 96, "mx")
-    y = torch.full((5, 64), 9.0, device="cuda")
+    x = dev(torch, activations(7, 96, 82)).bfloat16()
+    need = w4.f4_gemv_workspace_size(7, 64, 96, "mx")
+    y = torch.full((7, 64), 9.0, device="cuda")
     with pytest.raises(w4.W4Error, match="W4_ERR_WORKSPACE"):
         w4.f4_gemv(*w.planes, x, y=y,
                    workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
@@ -676,13 +676,14 @@ def test_two_host_threads(torch, w4):
     def work(seed, fmt):
         s = torch.cuda.Stream()
         with torch.cuda.stream(s):
-            w = random_matrix(torch, 1500, 544, fmt, seed)
-            x = dev(torch, activations(6, 544, seed + 1)).bfloat16()
+            w = random_matrix(torch, 6500, 544, fmt, seed)
+            x = dev(torch, activations(7, 544, seed + 1)).bfloat16()
             src = dev(torch, activations(150, 544, seed + 2)).bfloat16()
             want = None
             for i in range(40):
                 q = w4.f4_quantize(src, fmt)
                 got = [w4.f4_gemv(*w.planes, x), w4.f4_gemv(*w.planes, x[:1]),
+                       w4.f4_gemv(*w.planes, x[:4]),
                        w4.f4_mm(*w.planes, *q), q[0]]
                 s.synchronize()
                 if want is None:

@@ -16,7 +16,7 @@
 //              run in issue order.
 //   warps 2-5  epilogue: TMEM -> registers -> y; a thread owns one weight row,
 //              so a warp's stores of one token are contiguous.
-//   warps 6-   f4_gemv of few tokens: activation digits (below).
+//   warps 6-   f4_gemv in one kernel: activation digits (below).
 // When the tiles do not fill the GPU, a cluster of up to 6 CTAs splits a tile's
 // K; each CTA leaves its fp32 partial tile in shared memory and the CTAs sum
 // them through distributed shared memory in CTA order (deterministic, and no
@@ -52,13 +52,11 @@ constexpr int kEpiWarps = 4;
 constexpr int kDigitWarp0 = kEpiWarp0 + kEpiWarps;  // fused f4_gemv: more warps
 constexpr int kDigits = 8;      // base-8 digits of an activation
 constexpr int kMaxTokens = 8;   // f4_gemv
-constexpr int kFusedTokens = 3; // most tokens whose digits the product kernel makes itself
 
-// Tokens up to which f4_gemv is one kernel.  Three tokens of MX in one (us): 2560
-// x 4096 4.9, 19456 x 2560 9.4, 2560 x 9728 7.0; four with their digits made by a
-// kernel of their own 5.7, 8.7, 7.5, and in one 5.9, 10.8, 9.0.  NV looks for the
-// largest exponent first, so it stops at two: 5.5, 10.2, 8.2 against 6.3, 9.7, 8.2.
-constexpr int fused_tokens(int fmt) { return fmt == W4_F4_MX ? 3 : 2; }
+// Tokens up to which f4_gemv is one kernel whatever the sizes, and up to which it
+// may be where K is split as far as it goes (see one_kernel).
+constexpr int fused_tokens(int fmt) { return fmt == W4_F4_MX ? 5 : 4; }
+constexpr int most_fused_tokens(int fmt) { return fmt == W4_F4_MX ? 8 : 6; }
 constexpr int kMaxSplit = 6;    // CTAs of a cluster that share a tile's K
 constexpr size_t kSmemTwo = 113 * 1024;  // of each of two CTAs on an SM (228 KB, 1 KB reserved a CTA)
 
@@ -90,8 +88,8 @@ struct Cfg {
     static constexpr int nbars = 2 * stages + 2 * acc_stages + 1;
     static constexpr int bars = stages * stage_bytes;
     static constexpr int misc = bars + nbars * 8;      // TMEM base, abort flag
-    static constexpr int amax = misc + 16;             // fused f4_gemv: [warps][tokens] maxima
-    static constexpr size_t total = (size_t)amax + 8 * kFusedTokens * 4;
+    static constexpr int amax = misc + 16;             // fused f4_gemv: largest magnitude of each token
+    static constexpr size_t total = (size_t)amax + kMaxTokens * 4;
     static_assert(used_cols <= 256, "TMEM has 512 columns, for two CTAs");
     static_assert(stage_bytes % 1024 == 0, "operand tiles start on swizzle atoms");
     static_assert(total <= kSmemTwo, "shared memory of an SM, for two CTAs");
@@ -252,9 +250,9 @@ __device__ __forceinline__ void digits8(const uint4& raw, bool live, int emax, i
 // kernel
 // ---------------------------------------------------------------------------
 
-// Digit warps of the fused f4_gemv.  A CTA's share of HBM delivers a stage about
-// every 900 cycles, which two warps a token keep up with.
-constexpr int digit_warps(int bn) { return bn / kDigits * 2; }
+// Digit warps of the fused f4_gemv: two a token, as far as the registers of two
+// CTAs on an SM allow.
+constexpr int digit_warps(int bn) { return bn <= 48 ? bn / kDigits * 2 : 12; }
 
 // Whether CTAs of a grid without K slices work on several tiles each.
 __host__ __device__ constexpr bool many_tiles(int64_t tiles, int64_t ctas) { return tiles > ctas; }
@@ -294,6 +292,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
     uint64_t* drain = aempty + C::acc_stages;                      // last MMA complete
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::misc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::misc + 4);
+    [[maybe_unused]] uint32_t* amax = reinterpret_cast<uint32_t*>(smem + C::amax);  // [tokens]
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         w4::prefetch_tmap(&tm_a);
         if constexpr (!FUSED) w4::prefetch_tmap(&tm_b);
         for (int i = 0; i < C::stages; ++i) {
-            // the producer, and a digit warp for each token
+            // the producer, and a warp's arrival for each token
             w4::mbar_init(&full[i], FUSED ? 1 + p.M : 1);
             w4::mbar_init(&empty[i], 1);
         }
@@ -361,6 +360,8 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         }
         w4::mbar_init(drain, 1);
         *abort_flag = 0;
+        if constexpr (FUSED && FMT == W4_F4_NV)
+            for (int t = 0; t < p.M; ++t) amax[t] = 0u;
         w4::fence_mbar_init();
         for (int i = 0; i < pre; ++i) load_a(i, k_from(0) + i, tile_of(0));
     }
@@ -473,37 +474,34 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         }
     } else if (FUSED && warp >= kDigitWarp0) {
         // ---------------- activation digits ----------------
-        // Warp w makes the digits of token w mod M, of every `per`-th stage from
-        // w / M on: 8 rows of 128 bytes of the stage's token operand (one
-        // swizzle atom) and their scale words.
+        // The warps take the tokens of the stages in turn: 8 rows of 128 bytes of
+        // a stage's token operand (one swizzle atom) and their scale words.
         constexpr int kDigitWarps = digit_warps(BN);
-        const int w = warp - kDigitWarp0;
-        const int per = kDigitWarps / p.M;  // warps that share a token
-        const int t = w % p.M, turn = w / p.M;
         constexpr int kWordLanes = block_of(FMT) / 2;
+        const int w = warp - kDigitWarp0;
         pdl_wait();
-        const uint16_t* xt = p.x + (int64_t)t * p.K;
-        const int k_end = k_to(0) * BK < p.K ? k_to(0) * BK : p.K;
-        int emax = 0;
         if constexpr (FMT == W4_F4_NV) {
-            // the largest exponent of this CTA's k (its first tile's hold the
-            // others'), over all digit warps
-            volatile uint32_t* part = reinterpret_cast<volatile uint32_t*>(smem + C::amax);
-            for (int tt = 0; tt < p.M; ++tt) {
-                uint32_t m = 0;
-                for (int k = k_from(0) * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
-                    m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(p.x + (int64_t)tt * p.K + k))));
-                m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0) part[w * kFusedTokens + tt] = m;
+            // the largest magnitude of each token over this CTA's k (its first
+            // tile's hold the others')
+            constexpr int kTokens = BN / kDigits;
+            const int k_end = k_to(0) * BK < p.K ? k_to(0) * BK : p.K;
+            uint32_t m[kTokens] = {};
+#pragma unroll 2
+            for (int k = k_from(0) * BK + (w * 32 + lane) * 8; k < k_end; k += kDigitWarps * 32 * 8)
+#pragma unroll
+                for (int t = 0; t < kTokens; ++t)
+                    if (t < p.M)
+                        m[t] = max(m[t], amax8(__ldca(reinterpret_cast<const uint4*>(
+                                             p.x + (int64_t)t * p.K + k))));
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                m[t] = __reduce_max_sync(0xffffffffu, m[t]);
+                if (t < p.M && lane == 0) atomicMax(&amax[t], m[t]);
             }
             digit_barrier<BN>();
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kDigitWarps; ++i) m = max(m, part[i * kFusedTokens + t]);
-            emax = exp_field(m);
         }
-        // the activations of the warp's next stage are loaded before it works on
-        // the present one; the stages of one tile follow those of the tile before
+        // a warp's next activations are loaded before it works on the present
+        // ones; the stages of one tile follow those of the tile before
         const int total = p.whole * p.stages_k + (shared < tiles ? ke - kb : 0);
         // a tile's last stage is followed by the next one's first: kb, which is
         // 0 unless a shared tile follows the only whole one
@@ -511,40 +509,45 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
             while (ks >= p.stages_k) ks += kb - p.stages_k;
             return ks;
         };
-        auto load_x = [&](int i, int ks) {
+        auto load_x = [&](int i, int ks, int t) {
             const int k = ks * BK + lane * 8;
             if (i < total && k < p.K && W4_CHECK(k + 8 <= p.K && t < p.M, p.err))
-                return __ldca(reinterpret_cast<const uint4*>(xt + k));
+                return __ldca(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.K + k));
             return make_uint4(0u, 0u, 0u, 0u);
         };
-        if (turn < per) {  // (three tokens may leave a warp without work)
-            int ks_next = wrap(k_from(0) + turn);
-            uint4 next = load_x(turn, ks_next);
-            for (int it = turn; it < total; it += per) {
-                const uint4 raw = next;
-                const bool live = ks_next * BK + lane * 8 < p.K;
-                ks_next = wrap(ks_next + per);
-                next = load_x(it + per, ks_next);
-                uint32_t out[kDigits], word;
-                digits8<FMT>(raw, live, emax, lane, out, word);
-                const int s = it % C::stages;
-                if (!w4::mbar_wait(&empty[s], ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort_flag,
-                                   p.err))
-                    break;
-                uint8_t* rows = smem + s * C::stage_bytes + C::a_bytes + t * kDigits * kRowBytes;
+        const int stages_on = kDigitWarps / p.M, tokens_on = kDigitWarps % p.M;
+        int it_next = w / p.M, t_next = w % p.M;
+        int ks_next = wrap(k_from(0) + it_next);
+        uint4 next = load_x(it_next, ks_next, t_next);
+        while (it_next < total) {
+            const uint4 raw = next;
+            const int it = it_next, t = t_next;
+            const bool live = ks_next * BK + lane * 8 < p.K;
+            const int on = stages_on + (t + tokens_on >= p.M ? 1 : 0);
+            t_next += tokens_on - (t + tokens_on >= p.M ? p.M : 0);
+            it_next += on;
+            ks_next = wrap(ks_next + on);
+            next = load_x(it_next, ks_next, t_next);
+            uint32_t out[kDigits], word;
+            const int emax = FMT == W4_F4_NV ? exp_field(*(volatile uint32_t*)&amax[t]) : 0;
+            digits8<FMT>(raw, live, emax, lane, out, word);
+            const int s = it % C::stages;
+            if (!w4::mbar_wait(&empty[s], ((uint32_t)(it / C::stages) & 1u) ^ 1u, abort_flag, p.err))
+                break;
+            uint8_t* rows = smem + s * C::stage_bytes + C::a_bytes + t * kDigits * kRowBytes;
 #pragma unroll
-                for (int j = 0; j < kDigits; ++j)
-                    *reinterpret_cast<uint32_t*>(rows + j * kRowBytes + (((lane >> 2) ^ j) << 4) +
-                                                 (lane & 3) * 4) = out[j];
-                // scale rows 8 t .. 8 t + 7 of the word's tile
-                uint8_t* sc = smem + s * C::stage_bytes + C::a_bytes + C::b_bytes + C::sa_bytes +
-                              lane / kWordLanes * kTileBytes + t * kDigits * 16;
-                if (lane % kWordLanes < kDigits)
-                    *reinterpret_cast<uint32_t*>(sc + lane % kWordLanes * 16) = word;
-                w4::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) w4::mbar_arrive(&full[s]);
-            }
+            for (int j = 0; j < kDigits; ++j)
+                *reinterpret_cast<uint32_t*>(rows + j * kRowBytes + (((lane >> 2) ^ j) << 4) +
+                                             (lane & 3) * 4) = out[j];
+            // scale rows 8 t .. 8 t + 7 of the word's tile: rows r and r + 32
+            // share a 16-byte line
+            uint8_t* sc = smem + s * C::stage_bytes + C::a_bytes + C::b_bytes + C::sa_bytes +
+                          lane / kWordLanes * kTileBytes + t % 4 * kDigits * 16 + t / 4 * 4;
+            if (lane % kWordLanes < kDigits)
+                *reinterpret_cast<uint32_t*>(sc + lane % kWordLanes * 16) = word;
+            w4::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) w4::mbar_arrive(&full[s]);
         }
     } else {
         // ---------------- epilogue ----------------
@@ -558,11 +561,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         // NV: the factor that the digits of token t leave out
         auto factor = [&](int t) {
             if constexpr (FUSED) {
-                const volatile uint32_t* part = reinterpret_cast<const volatile uint32_t*>(smem + C::amax);
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < digit_warps(BN); ++i) m = max(m, part[i * kFusedTokens + t]);
-                return nv_factor(exp_field(m));
+                return nv_factor(exp_field(*(volatile uint32_t*)&amax[t]));
             } else {
                 return __ldca(p.row_factor + t);
             }
@@ -682,7 +681,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
 }
 
 // ---------------------------------------------------------------------------
-// f4_gemv of more tokens than fused_tokens: the digits in global memory
+// f4_gemv in two kernels (see one_kernel): the digits in global memory
 // ---------------------------------------------------------------------------
 
 constexpr int kDigitThreads = 256;
@@ -864,16 +863,38 @@ int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStre
     return launch_tiles<FMT, 64, kMm>(codes, qa, p, st);
 }
 
+// Whether the product makes its digits itself, every CTA those of its own k and so
+// all of them once for each 128 weight rows, instead of reading what a kernel of
+// their own made once.  us, in one and in two kernels:
+//   tokens               MX 4       MX 5       MX 6       NV 3       NV 4       NV 5
+//   2560 x 9728       6.1  7.3   6.4  7.4   6.5  7.4   6.7  8.1   6.9  8.2   7.4  8.3
+//   19456 x 2560      7.9  8.6   8.9  8.8   9.7  8.8   8.6  9.7   9.3  9.7  10.7 10.0
+//   128256 x 4096    45.8 45.8  47.6 47.1  49.7 47.1             49.4 49.9  52.0 49.9
+//   151936 x 2560    32.5 32.8  33.4 34.8  35.0 34.8  36.2 36.8  36.3 37.1  36.2 37.5
+// Up to fused_tokens it is one.  From there on the digits take the longer time, but
+// for the tiles that clusters of kMaxSplit share: few stages a CTA, and two launches
+// that count (MX at 8 tokens 1024 x 2560 4.3, 4.95; 2560 x 4096 5.15, 5.9; NV at 6
+// 2560 x 9728 7.65, 8.5).  At about 50 token stages a CTA both are equal (MX at 8
+// tokens 2560 x 9728, 56 of them, 7.65, 7.6); NV, which looks for the largest
+// magnitudes first, loses there (4096 x 14336 at 5 tokens, 50: 11.6, 11.0).
+bool one_kernel(int64_t M, int64_t N, int64_t K, int fmt) {
+    if (M <= fused_tokens(fmt)) return true;
+    const int64_t stages = ((K + BK - 1) / BK + kMaxSplit - 1) / kMaxSplit;
+    return M <= most_fused_tokens(fmt) &&
+           row_tiles(N) * kMaxSplit <= (int64_t)w4::sm_count() * 2 && stages * M <= (fmt == W4_F4_MX ? 50 : 45);
+}
+
 template <int FMT>
 int launch_fused(const uint8_t* codes, const Params& p, cudaStream_t st) {
-    if constexpr (fused_tokens(FMT) > 2)
-        if (p.M > 2) return launch_tiles<FMT, 32, kGemvFused>(codes, nullptr, p, st);
-    return launch_tiles<FMT, 16, kGemvFused>(codes, nullptr, p, st);
+    if (p.M <= 2) return launch_tiles<FMT, 16, kGemvFused>(codes, nullptr, p, st);
+    if (p.M <= 4) return launch_tiles<FMT, 32, kGemvFused>(codes, nullptr, p, st);
+    if constexpr (most_fused_tokens(FMT) > 6)
+        if (p.M > 6) return launch_tiles<FMT, 64, kGemvFused>(codes, nullptr, p, st);
+    return launch_tiles<FMT, 48, kGemvFused>(codes, nullptr, p, st);
 }
 
 template <int FMT>
 int launch_planes(const uint8_t* codes, const uint8_t* digits, const Params& p, cudaStream_t st) {
-    if (p.M <= 4) return launch_tiles<FMT, 32, kGemvPlanes>(codes, digits, p, st);
     if (p.M <= 6) return launch_tiles<FMT, 48, kGemvPlanes>(codes, digits, p, st);
     return launch_tiles<FMT, 64, kGemvPlanes>(codes, digits, p, st);
 }
@@ -965,9 +986,8 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     if (!w4::aligned16(codes) || !w4::aligned16(scales) || !w4::aligned16(x_bf16) ||
         !w4::aligned16(y) || (nv && bad_scalar(g)))
         return W4_ERR_ALIGN;
-    const bool fused = M <= fused_tokens(format);
     const GemvWs ws = gemv_ws(M, K, format);
-    if (!fused) {
+    if (M > fused_tokens(format)) {
         if (!workspace || ws_bytes < ws.total) return W4_ERR_WORKSPACE;
         if (!w4::aligned16(workspace)) return W4_ERR_ALIGN;
     }
@@ -978,7 +998,7 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     if (rc != W4_OK) return rc;
     p.b_rows = M * kDigits;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (fused) {
+    if (one_kernel(M, N, K, format)) {
         p.x = x_bf16;
         return nv ? launch_fused<W4_F4_NV>(codes, p, st) : launch_fused<W4_F4_MX>(codes, p, st);
     }
