@@ -93,7 +93,7 @@ def build_calls(force: bool = False) -> str:
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC"] + [f"-I{d}" for d in include] + \
           [src, "-o", CALLS, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu",
-           "-lc10", "-lc10_cuda"]
+           "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")

@@ -1,19 +1,20 @@
 // f4call.cpp -- the plain calls of the f4_* Python functions, without the
 // interpreter: the decode-sized operators take 2 to 6 us on the GPU, and checking
 // tensors and marshalling a C call in Python takes longer than that (a call of
-// f4_mm 11.5 us, f4_gemv 10.9; here 5 to 6).
+// f4_mm 11.5 us, f4_gemv 10.9; here 4).
 //
 // Every function takes what its Python namesake takes of a call with no output,
 // workspace or stream of the caller's.  It makes the binding's checks -- plain
 // CUDA tensors on the current device, types, exact shapes, contiguity -- and on
 // anything else, or on a status other than W4_OK, returns None; the Python
 // function then goes its own way, which says what is wrong.  Outputs come from
-// torch's allocator on the current stream.  The C entry points are handed over as
+// torch's allocator on the current stream, past its dispatcher (0.4 us a tensor),
+// which has nothing to add for a buffer that is written in full.  The C entry points are handed over as
 // addresses, so that this module works on whichever libw4 is loaded.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -84,7 +85,7 @@ bool out_type(PyObject* o, int& code, at::ScalarType& type) {
 }
 
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 void* stream(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
