@@ -342,9 +342,9 @@ int f4_mm(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N
           int64_t K, int format, const uint8_t *qa, const uint8_t *sa,
           const float *ga, int64_t M, void *y, int out_dtype, void *stream);
 
-/* Bytes of device workspace that f4_gemv needs (0 for up to 5 tokens
- * of MX and 4 of NV, whose digits never leave the kernel, and for sizes outside
- * its range). */
+/* Bytes of device workspace that f4_gemv needs on the current device (0 where
+ * the digits never leave the kernel -- up to 5 tokens of MX and 4 of NV, and some
+ * more for small weights -- and for sizes outside its range). */
 size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format);
 
 /* Decode GEMV: y[t][n] = g * sum_k (q * s)[n][k] * x[t][k] with bf16

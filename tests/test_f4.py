@@ -623,10 +623,10 @@ def test_weights_from_another_stream(torch, w4, fmt):
 
 
 def test_workspace_too_small_is_refused(torch, w4):
-    w = random_matrix(torch, 64, 96, "mx", 81)
+    w = random_matrix(torch, 6500, 96, "mx", 81)
     x = dev(torch, activations(7, 96, 82)).bfloat16()
-    need = w4.f4_gemv_workspace_size(7, 64, 96, "mx")
-    y = torch.full((7, 64), 9.0, device="cuda")
+    need = w4.f4_gemv_workspace_size(7, 6500, 96, "mx")
+    y = torch.full((7, 6500), 9.0, device="cuda")
     with pytest.raises(w4.W4Error, match="W4_ERR_WORKSPACE"):
         w4.f4_gemv(*w.planes, x, y=y,
                    workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))

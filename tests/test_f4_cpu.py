@@ -172,10 +172,10 @@ def test_mm_validation(lib):
 
 def test_gemv_validation(lib):
     from w4_quant_matmul_b200 import _lib as L
-    need = lib.f4_gemv_workspace_size(5, 256, 96, 1)
+    need = lib.f4_gemv_workspace_size(7, 256, 96, 1)
     assert need > 0 and lib.f4_gemv_workspace_size(2, 256, 96, 1) == 0
     names = ["codes", "scales", "g", "N", "K", "fmt", "x", "M", "y", "out", "ws", "nws", "st"]
-    ok = [FAKE, FAKE, FAKE, 256, 96, 1, FAKE, 5, FAKE, 0, FAKE, need, None]
+    ok = [FAKE, FAKE, FAKE, 256, 96, 1, FAKE, 7, FAKE, 0, FAKE, need, None]
 
     def call(**kw):
         return lib.f4_gemv(*[kw.get(n, v) for n, v in zip(names, ok)])

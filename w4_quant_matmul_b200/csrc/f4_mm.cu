@@ -970,9 +970,7 @@ int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N
 }
 
 size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format) {
-    if (!gemv_range(M, N, K) || !f4::known_format(format) ||
-        M <= fused_tokens(format))
-        return 0;
+    if (!gemv_range(M, N, K) || !f4::known_format(format) || one_kernel(M, N, K, format)) return 0;
     return gemv_ws(M, K, format).total;
 }
 
@@ -986,8 +984,9 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     if (!w4::aligned16(codes) || !w4::aligned16(scales) || !w4::aligned16(x_bf16) ||
         !w4::aligned16(y) || (nv && bad_scalar(g)))
         return W4_ERR_ALIGN;
+    const bool fused = one_kernel(M, N, K, format);
     const GemvWs ws = gemv_ws(M, K, format);
-    if (M > fused_tokens(format)) {
+    if (!fused) {
         if (!workspace || ws_bytes < ws.total) return W4_ERR_WORKSPACE;
         if (!w4::aligned16(workspace)) return W4_ERR_ALIGN;
     }
@@ -998,7 +997,7 @@ int f4_gemv(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t
     if (rc != W4_OK) return rc;
     p.b_rows = M * kDigits;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (one_kernel(M, N, K, format)) {
+    if (fused) {
         p.x = x_bf16;
         return nv ? launch_fused<W4_F4_NV>(codes, p, st) : launch_fused<W4_F4_MX>(codes, p, st);
     }
