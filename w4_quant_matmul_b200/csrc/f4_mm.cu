@@ -22,11 +22,11 @@
 // them through distributed shared memory in CTA order (deterministic, and no
 // workspace).  Otherwise CTAs are persistent and their accumulators double
 // buffered; f4_gemv, where they would take one or two tiles each, takes one and
-// splits the others' K so.  What bounds it: bytes from HBM for large streams, and for small
-// ones latency, of which about 4 us remain at any size: one HBM access, the MMAs'
-// completion, the sum over the cluster.  Tiles of 64 tokens at most: 128 were
-// slower wherever the CTA pairs are not faster still (2560 x 9728 at 256 tokens
-// 13.5 us against 12.6).
+// splits the others' K so.  What bounds it: bytes from HBM for large streams, and
+// for small ones latency, of which 3 to 4 us remain at any size: one HBM access,
+// the MMAs' completion, the sum over the cluster.  Tiles of 64 tokens at most: 128
+// were slower wherever the CTA pairs are not faster still (2560 x 9728 at 256
+// tokens 13.5 us against 12.6).
 //
 // f4_gemv keeps x exact to 22 bits of each block's largest magnitude without
 // leaving the 4-bit tensor cores: x is written as fixed point in eight base-8
@@ -36,7 +36,8 @@
 // once, whatever the number of tokens, and no CUDA core touches them: at 54
 // weights a cycle and SM, unpacking them there would take most of the issue slots
 // at one token and several times too many at eight.  lm_head 151936 x 2560 (MX):
-// 31.4 us at one token, 34.7 at eight (6590 and 5950 GB/s of weights).
+// 31.0 us at one token, 34.4 at eight (6670 and 6010 GB/s of weights).  That every
+// tile loads the digits of many tokens from L2 again costs nothing (34.8 without).
 #include <cuda_bf16.h>
 
 #include "f4_pair.cuh"
