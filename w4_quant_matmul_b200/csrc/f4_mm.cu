@@ -705,13 +705,24 @@ __global__ void __launch_bounds__(kDigitThreads)
     const int lane = threadIdx.x & 31;
     const uint16_t* xt = x + (int64_t)t * K;
 
+    const int64_t tiles_k = scale_tiles_k(K, FMT);
+    const int kpad = (int)tiles_k * 4 * block_of(FMT);
+    const int k = blockIdx.x * kDigitElems + threadIdx.x * 8;
+    const bool live = k < K;
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (live && W4_CHECK(k + 8 <= K, err)) raw = __ldca(reinterpret_cast<const uint4*>(xt + k));
+
     int emax = 0;  // NV: largest exponent field of the token
     if constexpr (FMT == W4_F4_NV) {
         __shared__ uint32_t part[kDigitThreads / 32];
         uint32_t m = 0;
-        for (int k = threadIdx.x * 8; k < K; k += kDigitElems)
-            m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(xt + k))));
-        m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll 4
+        for (int i = 1; i < (int)gridDim.x; ++i) {  // the other blocks' elements
+            const int other = blockIdx.x + i < gridDim.x ? blockIdx.x + i : blockIdx.x + i - gridDim.x;
+            const int ko = other * kDigitElems + threadIdx.x * 8;
+            if (ko < K) m = max(m, amax8(__ldca(reinterpret_cast<const uint4*>(xt + ko))));
+        }
+        m = __reduce_max_sync(0xffffffffu, max(m, amax8(raw)));
         if (lane == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
 #pragma unroll
@@ -720,15 +731,9 @@ __global__ void __launch_bounds__(kDigitThreads)
         if (blockIdx.x == 0 && threadIdx.x == 0) row_factor[t] = nv_factor(emax);
     }
 
-    const int64_t tiles_k = scale_tiles_k(K, FMT);
-    const int kpad = (int)tiles_k * 4 * block_of(FMT);
     // whole warps run or skip; in a warp that runs, the lanes past kpad only
     // take part in the shuffles
-    const int k = blockIdx.x * kDigitElems + threadIdx.x * 8;
     if (k - lane * 8 >= kpad) return;
-    const bool live = k < K;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (live && W4_CHECK(k + 8 <= K, err)) raw = __ldca(reinterpret_cast<const uint4*>(xt + k));
     uint32_t out[kDigits], word;
     digits8<FMT>(raw, live, emax, lane, out, word);
     if (live) {
