@@ -873,16 +873,16 @@ int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStre
 // all of them once for each 128 weight rows, instead of reading what a kernel of
 // their own made once.  us, in one and in two kernels:
 //   tokens               MX 4       MX 5       MX 6       NV 3       NV 4       NV 5
-//   2560 x 9728       6.1  7.3   6.4  7.4   6.5  7.4   6.7  8.1   6.9  8.2   7.4  8.3
-//   19456 x 2560      7.9  8.6   8.9  8.8   9.7  8.8   8.6  9.7   9.3  9.7  10.7 10.0
-//   128256 x 4096    45.8 45.8  47.6 47.1  49.7 47.1             49.4 49.9  52.0 49.9
-//   151936 x 2560    32.5 32.8  33.4 34.8  35.0 34.8  36.2 36.8  36.3 37.1  36.2 37.5
+//   2560 x 9728       6.1  7.3   6.4  7.4   6.5  7.4   6.5  8.0   6.8  8.0   7.4  8.15
+//   19456 x 2560      7.9  8.6   8.9  8.8   9.7  8.8   8.4  9.1   9.25 9.2  10.6  9.4
+//   128256 x 4096    45.8 45.8  47.6 47.1  49.7 47.1  48.6 49.0  49.2 48.8  52.1 49.0
+//   151936 x 2560    32.5 32.8  33.4 34.8  35.0 34.8  35.9 35.3  35.9 35.6  36.0 36.0
 // Up to fused_tokens it is one.  From there on the digits take the longer time, but
 // for the tiles that clusters of kMaxSplit share: few stages a CTA, and two launches
 // that count (MX at 8 tokens 1024 x 2560 4.3, 4.95; 2560 x 4096 5.15, 5.9; NV at 6
-// 2560 x 9728 7.65, 8.5).  At about 50 token stages a CTA both are equal (MX at 8
+// 2560 x 9728 7.6, 8.3).  At about 50 token stages a CTA both are equal (MX at 8
 // tokens 2560 x 9728, 56 of them, 7.65, 7.6); NV, which looks for the largest
-// magnitudes first, loses there (4096 x 14336 at 5 tokens, 50: 11.6, 11.0).
+// magnitudes first, loses there (4096 x 14336 at 5 tokens, 50: 11.6, 10.9).
 bool one_kernel(int64_t M, int64_t N, int64_t K, int fmt) {
     if (M <= fused_tokens(fmt)) return true;
     const int64_t stages = ((K + BK - 1) / BK + kMaxSplit - 1) / kMaxSplit;
