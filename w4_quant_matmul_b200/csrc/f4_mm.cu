@@ -885,9 +885,11 @@ int launch_mm(const uint8_t* codes, const uint8_t* qa, const Params& p, cudaStre
 // magnitudes first, loses there (4096 x 14336 at 5 tokens, 50: 11.6, 10.9).
 bool one_kernel(int64_t M, int64_t N, int64_t K, int fmt) {
     if (M <= fused_tokens(fmt)) return true;
+    (void)w4::check_device();  // sm_count knows the device from here on
     const int64_t stages = ((K + BK - 1) / BK + kMaxSplit - 1) / kMaxSplit;
-    return M <= most_fused_tokens(fmt) &&
-           row_tiles(N) * kMaxSplit <= (int64_t)w4::sm_count() * 2 && stages * M <= (fmt == W4_F4_MX ? 50 : 45);
+    const int64_t most = fmt == W4_F4_MX ? 50 : 45;  // token stages a CTA
+    return M <= most_fused_tokens(fmt) && stages * M <= most &&
+           row_tiles(N) * kMaxSplit <= (int64_t)w4::sm_count() * 2;
 }
 
 template <int FMT>
