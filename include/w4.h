@@ -400,6 +400,12 @@ int w4a8_gemv_blockdots(const uint8_t *codes, const uint16_t *d_f16,
                         int M, void *y, int out_dtype, int32_t *blockdots,
                         size_t bd_bytes, void *stream);
 
+/* Which of its two kernels f4_mm runs for M tokens and N weight rows on the
+ * current device: 1 for the CTA pairs, 0 for the 128 x 64 tiles, -1 for sizes
+ * outside its range (the rule that f4_mm itself evaluates, so that a test can
+ * tell which kernel its shapes reach). */
+int w4_test_f4_mm_pairs(int64_t M, int64_t N);
+
 /* Runs the bounded-wait routine that every pipelined kernel of this library
  * uses, on a wait that can never complete: one thread waits on an mbarrier
  * phase that nothing completes, for limit_ns nanoseconds of GPU global time,

@@ -62,6 +62,7 @@ SIGNATURES = {
     "f4_mm": ([_P, _P, _P, _I64, _I64, _INT, _P, _P, _P, _I64, _P, _INT, _P], _INT),
     "f4_gemv_workspace_size": ([_I64, _I64, _I64, _INT], ctypes.c_size_t),
     "f4_gemv": ([_P, _P, _P, _I64, _I64, _INT, _P, _INT, _P, _INT, _P, ctypes.c_size_t, _P], _INT),
+    "w4_test_f4_mm_pairs": ([_I64, _I64], _INT),
     "w4_test_wait_expiry": ([ctypes.c_uint64, _P], _INT),
     "w4a8_gemv_blockdots": ([_P, _P, _P, _I64, _I64, _P, _P, _P, _INT, _P, _INT, _P,
                              ctypes.c_size_t, _P], _INT),

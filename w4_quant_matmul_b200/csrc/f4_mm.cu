@@ -907,6 +907,12 @@ int launch_planes(const uint8_t* codes, const uint8_t* digits, const Params& p, 
     return launch_tiles<FMT, 64, kGemvPlanes>(codes, digits, p, st);
 }
 
+// Whether f4_mm runs the CTA pairs (f4_pair.cu): wide tiles for many tokens, unless
+// one round of 128 x 64 tiles covers y.
+bool pairs(int64_t M, int64_t N) {
+    return M > 64 && row_tiles(N) * ((M + 63) / 64) > w4::sm_count();
+}
+
 bool bad_scalar(const float* g) { return (reinterpret_cast<uintptr_t>(g) & 3u) != 0; }
 
 int fill(Params& p, const uint8_t* scales, const float* g, int64_t N, int64_t K, int format,
@@ -962,8 +968,7 @@ int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N
         return W4_ERR_ALIGN;
     int rc = w4::check_device();
     if (rc != W4_OK) return rc;
-    // wide tiles for CTA pairs, unless one round of 128 x 64 tiles covers y
-    if (row_tiles(N) * ((M + 63) / 64) > w4::sm_count() && M > 64) {
+    if (pairs(M, N)) {
         const PairArgs a{codes, scales, g, N, K, qa, sa, ga, M, y, w4::device_error_word()};
         return launch_pair(a, format, out_dtype, (cudaStream_t)stream);
     }
@@ -975,6 +980,12 @@ int f4_mm(const uint8_t* codes, const uint8_t* scales, const float* g, int64_t N
     p.b_rows = (int)M;
     return nv ? launch_mm<W4_F4_NV>(codes, qa, p, (cudaStream_t)stream)
               : launch_mm<W4_F4_MX>(codes, qa, p, (cudaStream_t)stream);
+}
+
+int w4_test_f4_mm_pairs(int64_t M, int64_t N) {
+    if (M < 1 || N < 1 || M > f4::kMaxRows || N > f4::kMaxRows) return -1;
+    (void)w4::check_device();  // sm_count knows the device from here on
+    return pairs(M, N) ? 1 : 0;
 }
 
 size_t f4_gemv_workspace_size(int64_t M, int64_t N, int64_t K, int format) {
