@@ -46,6 +46,24 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     }
 }
 
+// A sum's factor a * b, as two factors to apply one after the other: 1 and their
+// product where that is a normal number.  Elsewhere the product itself would lose its
+// bits or overflow although the sum brings the result back into range (a tensor
+// scale of 2^-100 times one of 2^-55, with sums up to 2^23 K): then the larger one
+// first.  What that leaves of the sum only leaves the range where the result does:
+// below 2^-126 the smaller one is less than 2^-63, above 2^128 more than 1.
+struct Factors {
+    float first, second;
+};
+__device__ __forceinline__ Factors factors(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    if (fabsf(p) >= 0x1p-126f && fabsf(p) <= 3.402823466e38f) return {1.0f, p};
+    return fabsf(a) >= fabsf(b) ? Factors{a, b} : Factors{b, a};
+}
+__device__ __forceinline__ float times(float v, const Factors& f) {
+    return v * f.first * f.second;
+}
+
 // Programmatic dependent launch.  Every f4 kernel waits for the kernel before it
 // ahead of its first access to global memory -- f4_gemv's product: to anything but
 // weights; the tensor scale: to anything but x, which the kernel before it never

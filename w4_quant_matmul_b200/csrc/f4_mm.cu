@@ -127,8 +127,10 @@ __device__ __forceinline__ void store_y(const Params& p, int64_t t, int n, float
 }
 
 // Four consecutive weight rows of token t.
-__device__ __forceinline__ void store_y4(const Params& p, int64_t t, int n, float4 v, float alpha) {
-    const float f[4] = {v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha};
+__device__ __forceinline__ void store_y4(const Params& p, int64_t t, int n, const float4& v,
+                                         const f4::Factors& scale) {
+    const float f[4] = {f4::times(v.x, scale), f4::times(v.y, scale), f4::times(v.z, scale),
+                        f4::times(v.w, scale)};
     if (p.N % 4 == 0 && n < p.N) {  // y's rows start on 4 elements: one vector
         if (!W4_CHECK(t >= 0 && t < p.M && n >= 0 && n + 4 <= p.N, p.err)) return;
         const int64_t at = t * p.N + n;
@@ -386,6 +388,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         tmem = *tmem_slot;
     }
 
+    Factors scale{1.0f, 1.0f};  // f4_mm, epilogue: both tensor scales (f4_gemv's are in the tiles)
     if (warp == 0) {
         // ---------------- TMA producer ----------------
         if (w4::elect_one()) {
@@ -554,10 +557,13 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
         // ---------------- epilogue ----------------
         const int quarter = warp & 3;  // the TMEM lanes this warp may read
         const int row = quarter * 32 + lane;
-        float alpha = 1.0f;
+        float alpha = 1.0f;  // the weights' tensor scale
         float* part = reinterpret_cast<float*>(smem);  // split K: [column][128] in the ring
         pdl_wait();
-        if constexpr (FMT == W4_F4_NV) alpha = GEMV ? __ldca(p.gw) : __fmul_rn(__ldca(p.gw), __ldca(p.ga));
+        if constexpr (FMT == W4_F4_NV) {
+            alpha = __ldca(p.gw);
+            if constexpr (!GEMV) scale = factors(alpha, __ldca(p.ga));
+        }
         if constexpr (FUSED && FMT == W4_F4_NV) digit_barrier<BN>();
         // NV: the factor that the digits of token t leave out
         auto factor = [&](int t) {
@@ -616,7 +622,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
                         if (partial)
                             part[(c + i) * BM + row] = v;
                         else if (t0 + i < p.M && n < p.N)
-                            store_y(p, t0 + i, n, v * alpha);
+                            store_y(p, t0 + i, n, times(v, scale));
                     }
                 }
             }
@@ -635,8 +641,6 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
             const int t0 = GEMV ? 0 : shared % p.tiles_m * BN;
             const int row = lane * 4, n = tn * BM + row;  // four weight rows a thread
             const int cols = p.M - t0 < BN ? p.M - t0 : BN;
-            float alpha = 1.0f;
-            if constexpr (FMT == W4_F4_NV && !GEMV) alpha = __fmul_rn(__ldca(p.gw), __ldca(p.ga));
             const uint32_t base = w4::smem_u32(smem) + row * 4;
             // columns split, split + splits, ...: one a warp and step; f4_mm has two
             // steps' loads in flight (four were no faster)
@@ -665,7 +669,7 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
                         sum.z += v[u][q].z;
                         sum.w += v[u][q].w;
                     }
-                    store_y4(p, t0 + cu, n, sum, alpha);
+                    store_y4(p, t0 + cu, n, sum, scale);
                 }
             }
         }
