@@ -59,6 +59,38 @@ def test_mm_of_any_two_tensor_scales(torch, w4, M, N, K, ew, ea):
                     float(np.float32(1.7 * 2.0 ** ea)))
 
 
+GEMV_PATHS = [(1, 300, 64), (4, 300, 2592), (6, 300, 2592), (7, 300, 64), (7, 6500, 64),
+              (1, 40000, 64), (8, 40000, 64)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMV_PATHS)
+@pytest.mark.parametrize("eg,ex", [(-20, 115), (-100, 120), (-100, -20), (-100, -45), (60, -126),
+                                   (100, -120), (100, -133), (90, 20), (20, 120)])
+def test_gemv_of_any_tensor_scale_and_activations(torch, w4, M, N, K, eg, ex):
+    """Integer activations times 2^ex (every digit exact)."""
+    w = random_matrix(torch, N, K, "nv", seed=5, g=float(np.float32(1.3 * 2.0 ** eg)))
+    rng = np.random.default_rng(7)
+    x = rng.integers(-8, 9, (M, K)) * 2.0 ** ex
+    if M > 1:
+        x[M - 1] = 0.0                              # a token whose sums are all zero
+    xt = dev(torch, x.astype(np.float32)).bfloat16()
+    x64 = host(xt.double())
+    y = host(w4.f4_gemv(*w.planes, xt, out_dtype=torch.float32))
+    want = x64 @ w.scaled.T
+    # below the normal numbers half a unit of 2^-149 for each of up to 6 K slices;
+    # the slices are added in fp32, so that the magnitudes have to stay inside it
+    bound = ref.gemv_bound(x64, w.scaled, K, "nv") + 6 * 2.0 ** -150
+    top = 2.0 ** 128 * (1 - 2.0 ** -24)
+    inside = np.abs(x64) @ np.abs(w.scaled).T + bound < top
+    over = np.abs(want) - bound > top
+    assert (np.abs(y.astype(np.float64)[inside] - want[inside]) <= bound[inside]).all()
+    assert not np.isfinite(y[over]).any()
+    if M > 1:
+        assert (y[M - 1] == 0).all()
+    y16 = w4.f4_gemv(*w.planes, xt)
+    assert torch.equal(y16.nan_to_num(nan=1.0), dev(torch, y).bfloat16().nan_to_num(nan=1.0))
+
+
 # ends of the block scales' range: sums that fp32 holds are exact (64 products of small
 # integers, quarters among them)
 @pytest.mark.parametrize("wb,ab", [(0, 254), (254, 0), (1, 253), (250, 10), (0, 127), (127, 0),

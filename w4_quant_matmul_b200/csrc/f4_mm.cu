@@ -565,14 +565,14 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
             if constexpr (!GEMV) scale = factors(alpha, __ldca(p.ga));
         }
         if constexpr (FUSED && FMT == W4_F4_NV) digit_barrier<BN>();
-        // NV: the factor that the digits of token t leave out
-        auto factor = [&](int t) {
-            if constexpr (FUSED) {
-                return nv_factor(exp_field(*(volatile uint32_t*)&amax[t]));
-            } else {
-                return __ldca(p.row_factor + t);
-            }
-        };
+        // f4_gemv, NV: what the digits of token `lane` leave out of its sums
+        Factors own{1.0f, 1.0f};
+        if constexpr (GEMV && FMT == W4_F4_NV) {
+            if (lane < p.M)
+                own = factors(FUSED ? nv_factor(exp_field(*(volatile uint32_t*)&amax[lane]))
+                                    : __ldca(p.row_factor + lane),
+                              alpha);
+        }
         for (int ti = 0; ti < units; ++ti) {
             const int tile = tile_of(ti);
             const bool partial = p.splits > 1 && (!GEMV || ti == p.whole);
@@ -599,8 +599,9 @@ __global__ void __launch_bounds__(threads_of(BN, MODE), 2)
                         for (int j = 6; j >= 0; --j)
                             v = fmaf(v, 0.125f, __uint_as_float(r[8 * h + j]));
                         if (t < p.M) {
-                            // (one at a time: their product could leave the range of fp32)
-                            if constexpr (FMT == W4_F4_NV) v = v * factor(t) * alpha;
+                            if constexpr (FMT == W4_F4_NV)
+                                v = times(v, Factors{__shfl_sync(0xffffffffu, own.first, t),
+                                                     __shfl_sync(0xffffffffu, own.second, t)});
                             if (partial)
                                 part[t * BM + row] = v;
                             else if (n < p.N)
