@@ -1,5 +1,6 @@
 """Scales at the ends of their ranges: tensor scales and activations whose product
-leaves the range of fp32 while the result does not, block scales 2^-127 and 2^127."""
+leaves the range of fp32 while the result does not, block scales 2^-127 and 2^127,
+scale bytes with the unused bit set."""
 import numpy as np
 import pytest
 
@@ -113,3 +114,25 @@ def test_gemv_extreme_block_scales(torch, w4, M, wb, ex):
     x = dev(torch, (rng.integers(-8, 9, (M, 64)) * 2.0 ** ex).astype(np.float32)).bfloat16()
     y = host(w4.f4_gemv(*w.planes, x, out_dtype=torch.float32))
     assert np.array_equal(y, f32(host(x.double()) @ w.values.T))
+
+
+def test_bit_7_of_a_scale_byte_is_not_read(torch, w4):
+    N, K = 300, 160
+    rng = np.random.default_rng(9)
+    scales = rng.integers(0, 128, (N, K // 16)).astype(np.uint8)   # NaN (127) among them
+    scales[:8] = 56
+    w = Matrix(torch, rng.integers(0, 16, (N, K)).astype(np.uint8), scales, "nv", 0.37)
+    a = random_matrix(torch, 20, K, "nv", 3)
+    high = lambda m: (m.planes[0], m.planes[1] | 0x80, m.planes[2])
+    x = dev(torch, rng.standard_normal((7, K))).bfloat16()
+    ids = dev(torch, np.array([0, 299, -1, 140]))
+    want = np.where(np.isnan(w.values), np.nan, w.values).astype(np.float32) * np.float32(0.37)
+    for planes, other in ((w.planes, a.planes), (high(w), high(a))):
+        got = host(w4.f4_dequantize(*planes, out_dtype=torch.float32))
+        assert np.array_equal(got, want, equal_nan=True)
+        rows = host(w4.f4_embed(*planes, ids, out_dtype=torch.float32))
+        assert np.array_equal(rows[[0, 1, 3]], want[[0, 299, 140]], equal_nan=True)
+        for f, rest in ((w4.f4_mm, other), (w4.f4_gemv, (x[:2],)), (w4.f4_gemv, (x,))):
+            y, ref_y = host(f(*planes, *rest, out_dtype=torch.float32)), \
+                host(f(*w.planes, *(a.planes if f is w4.f4_mm else rest), out_dtype=torch.float32))
+            assert np.array_equal(y, ref_y, equal_nan=True)

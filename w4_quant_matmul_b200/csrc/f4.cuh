@@ -41,7 +41,8 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
         // 2^-127 and 255 NaN
         return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
     } else {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
+        // bits 0-6 alone: the tensor cores read the byte as an unsigned number too
+        const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(byte & 0x7Fu), __NV_E4M3);
         return __half2float(__half(h));
     }
 }
