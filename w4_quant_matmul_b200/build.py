@@ -6,7 +6,9 @@ with the static CUDA runtime so the library is self-contained.
     python -m w4_quant_matmul_b200.build --debug  # libw4_debug.so (-DW4_DEBUG)
 
 The release build also compiles ``_f4call.so``, the plain calls of the f4_*
-functions as a Python extension (g++, torch's headers; no kernels in it).
+functions as a Python extension (no kernels in it).  That one needs g++ and a
+torch with CUDA; where they are missing the build says so and goes on, and those
+calls go through ctypes.
 
 The ptxas resource report (registers, spills, shared memory per kernel) is
 written to ``_build/ptxas.log``.
@@ -20,6 +22,7 @@ import re
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -81,11 +84,17 @@ def _compile(src: str, force: bool, debug: bool = False) -> tuple[str, str]:
 
 
 def build_calls(force: bool = False) -> str:
-    """Compile ``_f4call.so`` against the installed torch."""
+    """Compile ``_f4call.so`` against the installed torch; raises OSError or
+    RuntimeError, and leaves none, where that is not possible."""
     src = os.path.join(CSRC, CALLS_SOURCE)
     if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "w4.h")]):
         return CALLS
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch = os.path.dirname(spec.origin)
     nvcc = _nvcc()
     cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
     include = [INCLUDE, os.path.join(torch, "include"),
@@ -110,7 +119,11 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         calls = None if debug else ex.submit(build_calls, force)
         results = list(ex.map(lambda s: _compile(s, force, debug), SOURCES))
         if calls:
-            calls.result()
+            try:
+                calls.result()
+            except (OSError, RuntimeError) as e:
+                warnings.warn(f"{os.path.basename(CALLS)} is not built, calls of the f4 functions "
+                              f"take the slower way through ctypes: {e}")
     objs = [o for o, _ in results]
     with open(os.path.join(out_dir, "ptxas.log"), "w") as f:
         for src, (_, log) in zip(SOURCES, results):
