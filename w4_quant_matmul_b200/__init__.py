@@ -445,14 +445,23 @@ _ext = None
 
 
 def _calls():
-    """The extension, bound to the loaded library; False if it is not built."""
+    """The extension, bound to the loaded library; False if it is not built, or
+    not for this torch."""
     global _ext
     if _ext is None:
         import ctypes
+        from .build import calls_tag
         torch, lib = _torch(), load()
         try:
             from . import _f4call as ext
         except ImportError:
+            _ext = False
+            return False
+        if getattr(ext, "built_for", None) != calls_tag(torch.__version__):
+            import warnings
+            warnings.warn("_f4call.so was built for another torch or Python: run `python -m "
+                          "w4_quant_matmul_b200.build` (calls of the f4 functions take the "
+                          "slower way through ctypes)")
             _ext = False
             return False
         names = ("f4_tensor_scale", "f4_quantize", "f4_dequantize", "f4_embed", "f4_mm", "f4_gemv",

@@ -83,24 +83,48 @@ def _compile(src: str, force: bool, debug: bool = False) -> tuple[str, str]:
     return obj, r.stderr
 
 
+def calls_tag(torch_version: str) -> str:
+    """What the extension is compiled for: it inlines torch's C++ classes and
+    Python's, whose layouts go with their versions."""
+    return f"_f4call for torch {torch_version}, {sys.implementation.cache_tag};"
+
+
+def _torch_version(torch_dir: str) -> str:
+    """The installed torch's version, without the time that importing it takes."""
+    text = open(os.path.join(torch_dir, "version.py")).read()
+    m = re.search(r"^__version__ = ['\"](.+)['\"]", text, re.M)
+    if not m:
+        raise RuntimeError("torch/version.py names no version")
+    return m.group(1)
+
+
+def _built_for(path: str, tag: str) -> bool:
+    """Whether the extension at `path` carries this tag (its string constant)."""
+    with open(path, "rb") as f:
+        return tag.encode() in f.read()
+
+
 def build_calls(force: bool = False) -> str:
     """Compile ``_f4call.so`` against the installed torch; raises OSError or
     RuntimeError, and leaves none, where that is not possible."""
     src = os.path.join(CSRC, CALLS_SOURCE)
-    if not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "w4.h")]):
+    spec = importlib.util.find_spec("torch")
+    torch = os.path.dirname(spec.origin) if spec else None
+    tag = calls_tag(_torch_version(torch)) if torch else None
+    if (tag and not force and not _stale(CALLS, [src, os.path.join(INCLUDE, "w4.h")])
+            and _built_for(CALLS, tag)):
         return CALLS
     if os.path.exists(CALLS):
         os.remove(CALLS)
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
+    if not torch:
         raise RuntimeError("torch is not installed")
-    torch = os.path.dirname(spec.origin)
     nvcc = _nvcc()
     cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
     include = [INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC"] + [f"-I{d}" for d in include] + \
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f'-DW4_BUILT_FOR="{tag}"'] + \
+          [f"-I{d}" for d in include] + \
           [src, "-o", CALLS, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu",
            "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)

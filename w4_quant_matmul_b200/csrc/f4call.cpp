@@ -268,4 +268,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_f4call", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__f4call() { return PyModule_Create(&module); }
+// built_for: the torch and the Python of this build; the binding calls nothing else of
+// a module that was built for others.
+PyMODINIT_FUNC PyInit__f4call() {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", W4_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
