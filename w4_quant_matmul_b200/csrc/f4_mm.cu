@@ -741,12 +741,13 @@ __global__ void __launch_bounds__(kDigitThreads)
     if (k - lane * 8 >= kpad) return;
     uint32_t out[kDigits], word;
     digits8<FMT>(raw, live, emax, lane, out, word);
-    if (live) {
+    if (live && W4_CHECK(t < kMaxTokens && k + 8 <= K, err)) {
 #pragma unroll
         for (int j = 0; j < kDigits; ++j)
             *reinterpret_cast<uint32_t*>(codes + ((int64_t)(t * kDigits + j) * K + k) / 2) = out[j];
     }
-    if (lane % kWordLanes == 0 && k < kpad) {
+    if (lane % kWordLanes == 0 && k < kpad &&
+        W4_CHECK(t * kDigits + kDigits <= kRowTile && k / (4 * block_of(FMT)) < tiles_k, err)) {
 #pragma unroll
         for (int j = 0; j < kDigits; ++j)
             *reinterpret_cast<uint32_t*>(

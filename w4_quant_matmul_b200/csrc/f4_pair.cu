@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads)
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 const int tn = tile / p.tiles_m, tm = tile % p.tiles_m;
-                (void)W4_CHECK(tn < p.tiles_n, p.err);
+                (void)W4_CHECK(tn < p.tiles_n && tm < p.tiles_m, p.err);
                 const int sa_row = (tm * 2 + (int)rank) * p.tiles_k;
                 const int sb_row = tn * PN / kRowTile * p.tiles_k;
                 for (int ks = 0; ks < p.stages_k; ++ks, ++it) {
@@ -375,13 +375,16 @@ __global__ void __launch_bounds__(kThreads)
                 if (aligned) {
                     const int j = lane % pieces;
                     const bool in = n0 + (j + 1) * vec <= p.N;
-                    uint8_t* y = static_cast<uint8_t*>(p.y) +
-                                 ((int64_t)(t0 + lane / pieces) * p.N + n0 + j * vec) * esize;
+                    const int64_t at =
+                        ((int64_t)(t0 + lane / pieces) * p.N + n0 + j * vec) * esize;
+                    uint8_t* y = static_cast<uint8_t*>(p.y) + at;
 #pragma unroll
                     for (int i = 0; i < pieces; ++i) {
                         const int row = i * rows_step + lane / pieces;
                         const uint4 v = *reinterpret_cast<const uint4*>(st + stage_at<pieces>(row, j));
-                        if (in && t0 + row < p.M)
+                        if (in && t0 + row < p.M &&
+                            W4_CHECK(at >= 0 && at + (int64_t)i * rows_step * p.N * esize + 16 <=
+                                                    (int64_t)p.M * p.N * esize, p.err))
                             *reinterpret_cast<uint4*>(y + (int64_t)i * rows_step * p.N * esize) = v;
                     }
                 } else if (n0 + lane < p.N) {  // one column a lane
@@ -389,6 +392,7 @@ __global__ void __launch_bounds__(kThreads)
                     for (int row = 0; row < 32 && t0 + row < p.M; ++row) {
                         const uint8_t* v = st + stage_at<pieces>(row, lane / vec) + in_piece;
                         const int64_t o = (int64_t)(t0 + row) * p.N + n0 + lane;
+                        if (!W4_CHECK(o >= 0 && o < (int64_t)p.M * p.N, p.err)) continue;
                         if constexpr (f32)
                             static_cast<uint32_t*>(p.y)[o] = *reinterpret_cast<const uint32_t*>(v);
                         else

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const void* __restri
 #pragma unroll
         for (int off = kBlkLanes; off < kWordLanes; off <<= 1)
             word |= __shfl_xor_sync(0xffffffffu, word, off);
-        if (live) {
+        if (live && W4_CHECK(r >= 0 && r < R && k + kElems <= K, err)) {
             if constexpr (kOct == 2)
                 *reinterpret_cast<uint2*>(code_row + k / 2) = make_uint2(c[0], c[1]);
             else
@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int u = 0; u < kU; ++u) {
         const int k = k0 + u * kSpan;
         if (k >= K) break;
+        if (!W4_CHECK(t >= 0 && t < T && k + kElems <= K, err)) break;
         float v[kElems];
 #pragma unroll
         for (int i = 0; i < kElems; i += 4) from_e2m1x4(q[u] >> (4 * i), v + i);
