@@ -280,7 +280,7 @@ int w4a8_mmq_static(const uint8_t *codes, const uint16_t *d_f16,
  *   W4_F4_MX  blocks of 32, s = 2^(byte - 127), byte 255 = NaN (the OCP
  *             Microscaling MXFP4 format: e8m0 scales)
  *   W4_F4_NV  blocks of 16, s = the e4m3 number of the byte (bits 0-6; 127 =
- *             NaN), and one fp32 scale g for the whole matrix
+ *             NaN; bit 7 is not read), and one fp32 scale g for the whole matrix
  * The scale plane is stored as the tensor cores read it, in tiles of 128 rows
  * x 4 blocks (512 bytes), row tiles outermost: the scale of row r, block b is
  * byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
@@ -309,9 +309,9 @@ int f4_tensor_scale(const void *x, int in_dtype, int64_t R, int64_t K, float *g,
  *       q = e2m1(x * 2^-e); amax = 0 gives byte 0
  *   NV: s = e4m3(amax / (6 * g)); q = e2m1(x * (1 / (s * g))), or 0 if s * g = 0
  * where e4m3 and e2m1 round to nearest even and saturate at 448 and 6; zeros
- * keep the sign of x.  g: device fp32 scalar in [2^-100, 2^100] for NV (from
- * f4_tensor_scale or from calibration; elements beyond 2688 * g saturate), not
- * read for MX (may be NULL).  A block that holds a NaN or an infinity gets
+ * keep the sign of x.  g: device fp32 scalar in [2^-100, 2^117] for NV (what
+ * f4_tensor_scale gives, or from calibration; elements beyond 2688 * g saturate),
+ * not read for MX (may be NULL).  A block that holds a NaN or an infinity gets
  * codes 0 and the NaN scale.  The whole scale plane is written, padding too.
  * R <= 2^24; R == 0 or K == 0 enqueues nothing. */
 int f4_quantize(const void *x, int in_dtype, int64_t R, int64_t K, int format,
@@ -336,6 +336,7 @@ int f4_embed(const uint8_t *codes, const uint8_t *scales, const float *g,
  *   y[t][n] = gw * ga * sum_k (q * s)_w[n][k] * (q * s)_a[t][k]
  * accumulated in fp32.  codes, scales, g: the weights [N][K]; qa, sa, ga: the
  * activations [M][K] (f4_quantize), both of `format`; y: [M][N] of out_dtype.
+ * gw * ga itself may leave the range of fp32 where the results do not.
  * 1 <= M <= 2^24, 1 <= N <= 2^24, 32 <= K <= 131072.  A NaN scale makes its
  * row or column NaN. */
 int f4_mm(const uint8_t *codes, const uint8_t *scales, const float *g, int64_t N,

@@ -677,14 +677,23 @@ def f4_mm(codes, scales, g, qa, sa, ga, out_dtype=None, y=None, stream=None):
 
 
 def f4_gemv_workspace_size(M: int, N: int, K: int, format="mx") -> int:
+    """Bytes of workspace that f4_gemv needs on the current device; 0 where it needs
+    none."""
     return int(load().f4_gemv_workspace_size(M, N, K, _f4_format(format)))
 
 
 def f4_gemv(codes, scales, g, x, out_dtype=None, y=None, workspace=None, stream=None):
     """y[M,N] = x[M,K] W^T for 1 <= M <= 8 from 4-bit weight planes and bf16
-    activations (not quantised to 4 bits).  workspace: optional uint8 1-D device
-    tensor of at least f4_gemv_workspace_size(M, N, K, format) bytes (allocated
-    here when omitted)."""
+    activations.  x is not quantised to 4 bits, but held in fixed point block by
+    block (32 k for MX, 16 for NV): to 2^-22 of the block's largest magnitude, so that
+    elements above 2^-14 of it are exact (NV: a block below 2^-17 of the token's
+    largest is held as if it were of that size).  The weight planes are read before
+    the kernel launched just before on the stream has ended: a kernel that writes them
+    must not be that one if it lets its successor start early (programmatic dependent
+    launch; f4_quantize and copies do not).  workspace:
+    optional uint8 1-D device tensor of at least f4_gemv_workspace_size(M, N, K,
+    format) bytes (allocated here when omitted); calls that can overlap on the GPU
+    need one each."""
     if y is None and workspace is None and stream is None and (_ext or _calls()):
         out = _ext.gemv(codes, scales, g, x, out_dtype)
         if out is not None:

@@ -23,10 +23,15 @@
 // workspace).  Otherwise CTAs are persistent and their accumulators double
 // buffered; f4_gemv, where they would take one or two tiles each, takes one and
 // splits the others' K so.  What bounds it: bytes from HBM for large streams, and
-// for small ones latency, of which 3 to 4 us remain at any size: one HBM access,
-// the MMAs' completion, the sum over the cluster.  Tiles of 64 tokens at most: 128
-// were slower wherever the CTA pairs are not faster still (2560 x 9728 at 256
-// tokens 13.5 us against 12.6).
+// latency for small ones: one HBM access, the MMAs' completion, the sum over the
+// cluster.  Above the time of its bytes a GEMV of one token takes 3 to 3.5 us (2560 x
+// 4096 3.8, NV 4.25), a product of up to 64 tokens 3.5 to 6 (2560 x 4096 at 16 tokens
+// 4.8, 6151 x 2592 at 33 7.2: more columns pass through the cluster's sum), one of 256
+// tokens 8 (2560 x 9728 10.7: every weight tile is read from L2 once for each 64
+// tokens, 79 MB), NV GEMVs with the digit kernel in front 6.5 (2560 x 9728 at eight
+// tokens 8.6).  Tiles of 64 tokens at most: of 128 they were slower wherever the CTA
+// pairs are not faster still (2560 x 9728 at 256 tokens 13.5 us against 12.6, both
+// with an earlier split of K).
 //
 // f4_gemv keeps x exact to 22 bits of each block's largest magnitude without
 // leaving the 4-bit tensor cores: x is written as fixed point in eight base-8
@@ -914,7 +919,18 @@ int launch_planes(const uint8_t* codes, const uint8_t* digits, const Params& p, 
 }
 
 // Whether f4_mm runs the CTA pairs (f4_pair.cu): wide tiles for many tokens, unless
-// one round of 128 x 64 tiles covers y.
+// one round of 128 x 64 tiles covers y.  us of the 128 x 64 tiles and of the pairs, NV;
+// the rule takes the pairs from | on:
+//   tokens               65           128           256           448           512          1024
+//   2560 x 4096      7.1  8.4      7.6  8.8      8.6  8.9      9.9  9.2  |  11.3  9.2     16.0   9.9
+//   2560 x 9728      9.1 15.4      9.7 15.9     11.5 15.9     14.1 16.0  |  19.4 16.0     30.2  16.8
+//   6144 x 2560      8.3  7.2      8.3  7.5  |   9.2  7.6     12.4  8.2     12.4  8.2     17.1  11.8
+//   19456 x 2560  | 16.5 16.1     14.4 12.6     17.3 12.2     21.5 15.5     24.8 15.7     45.5  29.0
+//   50257 x 2560  | 27.8 37.4     20.6 30.3     33.0 30.3     55.9 59.0     62.1 60.6    119.7 117.0
+// (MX alike.)  It is off where it turns a few tokens too late (6144 x 2560 at 65 to 192
+// tokens up to a fifth, 2560 x 4096 at 384 and 448 a tenth) and where absent tokens
+// fill the pairs' 256-token tiles and their rows of y start off 16 bytes (50257 rows
+// at 65 to 192 and at 384 tokens: a fifth to a half more).
 bool pairs(int64_t M, int64_t N) {
     return M > 64 && row_tiles(N) * ((M + 63) / 64) > w4::sm_count();
 }

@@ -1,7 +1,7 @@
 // f4call.cpp -- the plain calls of the f4_* Python functions, without the
 // interpreter: the decode-sized operators take 2 to 6 us on the GPU, and checking
 // tensors and marshalling a C call in Python takes longer than that (a call of
-// f4_mm 11.5 us, f4_gemv 10.9; here 4).
+// f4_mm 11.5 us, f4_gemv 10.9; here 4.0 and 3.9).
 //
 // Every function takes what its Python namesake takes of a call with no output,
 // workspace or stream of the caller's.  It makes the binding's checks -- plain
